@@ -25,8 +25,10 @@ EXPORTED = ["enc_create", "enc_forward", "enc_output_positions", "enc_get_status
             "enc_frontend_create", "enc_frontend_log_mel", "enc_frontend_destroy",
             "enc_cache_create", "enc_forward_cached", "enc_cache_size", "enc_cache_destroy", "enc_cache_content_keys",
             "enc_clip_flops", "enc_shard_plan", "enc_selftest_timeout", "enc_check_guards",
-            "enc_guard_selftest"]
+            "enc_guard_selftest", "enc_fp8_scale_pitch", "enc_quantize_fp8", "enc_norm_fp8", "enc_linear_fp8"]
 ENC_FLAG_GUARD = 1
+ENC_NORM_RMS, ENC_NORM_LAYER = 0, 1
+ENC_FP8_OUT_BF16, ENC_FP8_OUT_FP32, ENC_FP8_OUT_FP8, ENC_FP8_OUT_RESID = range(4)
 
 KERNEL_CLASSES = ["mel", "conv1", "conv2", "ln", "qkv", "attn", "out", "fc1", "fc2", "final", "proj1", "proj2",
                   "zero"]
@@ -131,6 +133,18 @@ def load_library(path: str = LIB_PATH):
     lib.enc_shard_plan.argtypes = [ctypes.POINTER(EncConfig), i32p, ctypes.c_int32, ctypes.c_int32, i32p, i32p, i32p,
                                    ctypes.POINTER(ctypes.c_double)]
     lib.enc_shard_plan.restype = ctypes.c_int
+    lib.enc_fp8_scale_pitch.argtypes = [ctypes.c_int32]
+    lib.enc_fp8_scale_pitch.restype = ctypes.c_int32
+    lib.enc_quantize_fp8.argtypes = [_VP, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _VP, _VP,
+                                     _VP]
+    lib.enc_quantize_fp8.restype = ctypes.c_int
+    lib.enc_norm_fp8.argtypes = [ctypes.c_int32, _VP, ctypes.c_int32, ctypes.c_int64, _VP, ctypes.c_int32,
+                                 ctypes.c_int64, _VP, _VP, ctypes.c_float, ctypes.c_int32, ctypes.c_int32, _VP,
+                                 ctypes.c_int64, _VP, _VP, _VP]
+    lib.enc_norm_fp8.restype = ctypes.c_int
+    lib.enc_linear_fp8.argtypes = [_VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_int32, ctypes.c_int32, _VP, _VP]
+    lib.enc_linear_fp8.restype = ctypes.c_int
     _LIB = lib
     return lib
 
@@ -355,6 +369,168 @@ def attention_bf16(qkv, cu, max_n, n_heads, out=None, status=None, stream=None):
                                              int(max_n), int(n_heads), _ptr(status), _stream_handle(stream)),
            "enc_attention_bf16")
     return out
+
+
+# ------------------------------------------------------ 8-bit (e4m3) operators
+def fp8_scale_pitch(cols: int) -> int:
+    """Bytes of one row of a scale matrix: ceil(cols / 128) rounded up to a multiple of four."""
+    return (int(cols) + 511) // 512 * 4
+
+
+def _expect(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _fp8_call(device, stream, fresh, call):
+    """call(stream handle) with `device` current. stream=None is the device's current stream;
+    tensors allocated here (`fresh`) are marked as used on a stream given by the caller."""
+    import torch
+    _expect(device.type == "cuda", "the tensors must be on a CUDA device")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _fp8_call(device, stream, fresh, call)
+    if stream is None:
+        return call(torch.cuda.current_stream().cuda_stream)
+    if fresh:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream))
+        for t in fresh:
+            t.record_stream(s)
+    return call(_stream_handle(stream))
+
+
+def _row_stride(t, device, what: str):
+    """(enc_dtype, row stride) of a bf16 or fp32 matrix whose rows are contiguous."""
+    import torch
+    _expect(t.dtype in (torch.bfloat16, torch.float32) and t.dim() == 2 and t.device == device
+            and (t.stride(1) == 1 or t.shape[1] <= 1),
+            f"{what} must be a bf16 or fp32 matrix with contiguous rows on {device}")
+    return (ENC_DTYPE_BF16 if t.dtype == torch.bfloat16 else ENC_DTYPE_FP32,
+            t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _fp8_matrix(q, scales, rows, cols, device, what: str):
+    """Check an e4m3 matrix with block scales (None: allocate it); returns (q, scales, the new ones)."""
+    import torch
+    fresh = []
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
+        fresh.append(q)
+    if scales is None:
+        scales = torch.empty((rows, fp8_scale_pitch(cols)), dtype=torch.float8_e8m0fnu, device=device)
+        fresh.append(scales)
+    _expect(q.dtype == torch.float8_e4m3fn and q.shape == (rows, cols) and q.is_contiguous() and q.device == device,
+            f"{what} must be a contiguous float8_e4m3fn [{rows}, {cols}] tensor on {device}")
+    _expect(scales.dtype in (torch.float8_e8m0fnu, torch.uint8) and scales.shape == (rows, fp8_scale_pitch(cols))
+            and scales.is_contiguous() and scales.device == device,
+            f"the scales of {what} must be a contiguous float8_e8m0fnu [{rows}, {fp8_scale_pitch(cols)}] tensor on "
+            f"{device}")
+    return q, scales, fresh
+
+
+def _fp32_vector(v, n, device, what: str):
+    import torch
+    _expect(v is None or (v.dtype == torch.float32 and v.shape == (n,) and v.is_contiguous() and v.device == device),
+            f"{what} must be a contiguous fp32 [{n}] tensor on {device}")
+
+
+def quantize_fp8(x, q=None, scales=None, stream=None):
+    """Rows of x [rows, cols] (bf16 or fp32, cols a multiple of 16) as e4m3 with a power-of-two
+    scale for each block of 128 columns (enc_quantize_fp8).
+
+    Returns (q float8_e4m3fn [rows, cols], scales float8_e8m0fnu [rows, fp8_scale_pitch(cols)]):
+    element (r, c) stands for q[r, c] * scales[r, c // 128].
+    """
+    dtype, ldx = _row_stride(x, x.device, "x")
+    rows, cols = x.shape
+    q, scales, fresh = _fp8_matrix(q, scales, rows, cols, x.device, "q")
+    lib = load_library()
+    _check(_fp8_call(x.device, stream, fresh, lambda s: lib.enc_quantize_fp8(
+        x.data_ptr(), dtype, ldx, rows, cols, q.data_ptr(), scales.data_ptr(), s)), "enc_quantize_fp8")
+    return q, scales
+
+
+def norm_fp8(x, gamma, beta=None, delta=None, kind="rms", eps=1e-5, x_out=None, q=None, scales=None, stream=None):
+    """RMS norm (kind "rms") or LayerNorm ("layer") of the residual stream x [rows, d] (bf16 or
+    fp32) after the addition of delta [rows, d] (bf16, fp32 or None), as e4m3 with block scales
+    (enc_norm_fp8).
+
+    Returns (q, scales, x_out): x_out is the stream after the addition, in x's type; without a
+    delta it is x itself, and x_out=x updates the stream in place. gamma, beta: fp32 [d].
+    """
+    import torch
+    _expect(kind in ("rms", "layer"), 'kind must be "rms" or "layer"')
+    dev = x.device
+    dtype, ldx = _row_stride(x, dev, "x")
+    rows, d = x.shape
+    _expect(gamma is not None, "gamma is required")
+    _fp32_vector(gamma, d, dev, "gamma")
+    _fp32_vector(beta, d, dev, "beta")
+    q, scales, fresh = _fp8_matrix(q, scales, rows, d, dev, "q")
+    ddtype, ldd = ENC_DTYPE_BF16, d
+    if delta is not None:
+        ddtype, ldd = _row_stride(delta, dev, "delta")
+        _expect(delta.shape == x.shape, "delta must have x's shape")
+        if x_out is None:
+            x_out = torch.empty((rows, d), dtype=x.dtype, device=dev)
+            fresh.append(x_out)
+    ldxo = d
+    if x_out is not None:
+        odtype, ldxo = _row_stride(x_out, dev, "x_out")
+        _expect(odtype == dtype and x_out.shape == x.shape, "x_out must have x's shape and type")
+    lib = load_library()
+    _check(_fp8_call(dev, stream, fresh, lambda s: lib.enc_norm_fp8(
+        ENC_NORM_RMS if kind == "rms" else ENC_NORM_LAYER, x.data_ptr(), dtype, ldx, _ptr(delta), ddtype, ldd,
+        gamma.data_ptr(), _ptr(beta), eps, rows, d, _ptr(x_out), ldxo, q.data_ptr(), scales.data_ptr(), s)),
+        "enc_norm_fp8")
+    return q, scales, x if x_out is None else x_out
+
+
+def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, out_scales=None, resid=None, gelu=False,
+               status=None, stream=None):
+    """act(A W^T + bias) of e4m3 matrices with block scales (as quantize_fp8 and norm_fp8 give
+    them), a [M, K] and w [N, K], K and N multiples of 16 (enc_linear_fp8).
+
+    The result's type is out's, or out_dtype ("bf16" when neither is given, "fp32" or "fp8"):
+    returns out, or (out, out_scales) for e4m3. With resid (fp32 [M, N]) the product and the
+    bias are added to it instead, and resid is returned. bias: fp32 [N].
+    """
+    import torch
+    dev = a.device
+    M, K = a.shape
+    N = w.shape[0]
+    _fp8_matrix(a, a_scales, M, K, dev, "a")
+    _fp8_matrix(w, w_scales, N, K, dev, "w")
+    _fp32_vector(bias, N, dev, "bias")
+    fresh = []
+    if resid is not None:
+        _expect(out is None and out_dtype is None and out_scales is None and not gelu,
+                "resid takes no out, out_dtype, out_scales or gelu")
+        _expect(resid.dtype == torch.float32 and resid.shape == (M, N) and resid.is_contiguous()
+                and resid.device == dev, f"resid must be a contiguous fp32 [{M}, {N}] tensor on {dev}")
+        kind, dst = ENC_FP8_OUT_RESID, resid
+    else:
+        types = {"bf16": (ENC_FP8_OUT_BF16, torch.bfloat16), "fp32": (ENC_FP8_OUT_FP32, torch.float32),
+                 "fp8": (ENC_FP8_OUT_FP8, torch.float8_e4m3fn)}
+        if out_dtype is None:
+            out_dtype = "bf16" if out is None else {t: n for n, (_, t) in types.items()}.get(out.dtype)
+        _expect(out_dtype in types, 'the output type must be "bf16", "fp32" or "fp8"')
+        kind, tdt = types[out_dtype]
+        if kind == ENC_FP8_OUT_FP8:
+            out, out_scales, fresh = _fp8_matrix(out, out_scales, M, N, dev, "out")
+        else:
+            _expect(out_scales is None, "out_scales belong to an e4m3 output")
+            if out is None:
+                out = torch.empty((M, N), dtype=tdt, device=dev)
+                fresh.append(out)
+            _expect(out.dtype == tdt and out.shape == (M, N) and out.is_contiguous() and out.device == dev,
+                    f"out must be a contiguous {out_dtype} [{M}, {N}] tensor on {dev}")
+        dst = out
+    lib = load_library()
+    _check(_fp8_call(dev, stream, fresh, lambda s: lib.enc_linear_fp8(
+        a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), _ptr(bias), dst.data_ptr(),
+        _ptr(out_scales), kind, M, N, K, 1 if gelu else 0, _ptr(status), s)), "enc_linear_fp8")
+    return (out, out_scales) if kind == ENC_FP8_OUT_FP8 else dst
 
 
 class Frontend:

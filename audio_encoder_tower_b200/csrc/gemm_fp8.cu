@@ -1,0 +1,507 @@
+// tcgen05 GEMM on e4m3 operands with a power-of-two scale for each block of 128
+// elements along K, fp32 accumulation in TMEM, fused epilogues:
+//
+//   out[M, N] = act(sum_kb 2^(ea[m, kb] + ew[n, kb]) sum_{k in kb} A[m, k] W[n, k] + bias[n])
+//
+// The tensor cores apply the scales themselves (kind::mxf8f6f4, one e8m0 scale per
+// row and 32 elements of K): the block's scale is used by the four MMAs of K = 32
+// that make up a block, so the accumulator needs no correction between blocks.
+//
+// Where the scales live. The MMA reads them from TMEM: lane l, column c of a
+// four-column group holds, in four bytes, the scales of row 32 c + l, repeated in
+// all four lane quarters; the instruction descriptor picks the byte. Four
+// consecutive blocks of a row are one 32-bit word of the caller's scale matrix,
+// so one word per row serves K = 512 and the byte index is the block modulo four.
+// A warp gathers the words into shared memory (16 bytes per lane: rows l, l + 32,
+// l + 64, l + 96) and the MMA thread copies them to TMEM with tcgen05.cp.
+#include <cudaTypedefs.h>
+
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace enc {
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far above any legitimate wait
+constexpr int kBK = 128;                           // K elements (and bytes) per stage: one scale block
+constexpr uint32_t kUnitScale = 0x7F7F7F7Fu;       // scales of rows outside the matrix: 2^0
+
+// Instruction descriptor, kind::mxf8f6f4: fp32 accumulator, e4m3 A and B, both
+// K-major, e8m0 scales; `id` is the byte (0..3) of the scale words to use.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
+  return (static_cast<uint32_t>(n >> 3) << 17)     // N / 8
+         | (1u << 23)                              // scale type: e8m0
+         | (static_cast<uint32_t>(m >> 7) << 27);  // M / 128
+}
+__device__ __forceinline__ uint32_t idesc_scale_id(uint32_t id) { return (id << 4) | (id << 29); }   // B, A
+
+// D[tmem of both CTAs] (+)= (A * scales) (B * scales)^T, M = 256 over the pair.
+__device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::
+          "r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 32 rows of 16 bytes of shared memory (512 contiguous bytes) to four TMEM columns,
+// repeated in the four lane quarters; each CTA of the pair copies its own.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Shared-memory descriptor of those 512 bytes: no swizzle, 8-row core matrices of
+// 16-byte rows, 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// --------------------------------------------------------------- shape of the kernel
+// A cluster of two CTAs computes 256 x 256 tiles (M = 256 over the pair). CTA r holds
+// rows 128 r .. of the A tile and rows 128 r .. of the W tile in a ring of 32 KB stages.
+//   warp 0   TMA producer;  warp 1 (first CTA)  MMA issuer;  warp 2  scales
+//   warps 3..10  epilogue: warps of a TMEM lane quarter split the tile's columns
+// TMEM has 512 columns: two accumulators of 256 and the scales do not fit side by side.
+// The accumulators overlap instead, by 32 columns: 0..255 and 224..479, scales from
+// 480. A tile's MMAs may start once the epilogue has read the 32 shared columns of the
+// tile before, which it therefore reads first; the rest of its work still overlaps the
+// next tile's MMAs.
+constexpr int kEpiWarp0 = 3, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kStages = 5;
+constexpr uint32_t kOperandBytes = 128 * kBK;          // per stage: this CTA's 128 rows of A, and of W
+constexpr uint32_t kTmemCols = 512, kAcc1 = 224, kScaleCol = 480, kScaleSlotCols = 12;
+constexpr uint32_t kScaleSlotBytes = 3 * 512;          // A: 128 rows, W: 256 rows
+constexpr int kScaleSlots = 2;
+constexpr size_t kSmemBytes = 1024 + kStages * (size_t)(2 * kOperandBytes) + kEpiWarps * (size_t)4096 +
+                              kScaleSlots * kScaleSlotBytes + 512;
+
+// Work units: tiles of 256 x 256 in row-major order, the last `tail` of them as two
+// halves of 128 columns, so that a last wave under half full keeps more SMs busy. A last
+// column tile of at most 128 columns is one narrow unit. An element's K order is the
+// same in each.
+struct Unit {
+  int m0, n0, width;
+};
+__device__ __forceinline__ Unit unit_at(const GemmFp8Params& p, int u) {
+  const int nfull = p.num_tiles - p.tail;
+  const int h = u - nfull, tile = h < 0 ? u : nfull + (h >> 1);
+  Unit t{(tile / p.tiles_n) * 256, (tile % p.tiles_n) * 256, 256};
+  if (h >= 0) { t.n0 += (h & 1) * 128; t.width = 128; }
+  if (p.N - t.n0 <= 128) t.width = 128;
+  return t;
+}
+
+// Word of scales (blocks 4 g .. 4 g + 3) of a row; rows outside the matrix scale by 1.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int pitch, int row, int rows, int g) {
+  return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(s + (int64_t)row * pitch) + g) : kUnitScale;
+}
+
+__device__ __forceinline__ float4 bias4(const GemmFp8Params& p, int c) {
+  if (p.bias && c < p.N) return __ldg(reinterpret_cast<const float4*>(p.bias + c));   // N is a multiple of 16
+  return make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// Epilogue of 32 rows x `cols` columns (from tile column c_first of the unit) by one warp.
+// `release` is called once, as soon as the columns shared with the other accumulator
+// have been read. Chunks run upwards or, with `down`, downwards, so that those come first.
+template <int kEpi, typename Release>
+__device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0, int cols,
+                                         uint32_t taddr, bool down, uint8_t* stage, int lane, Release&& release) {
+  if constexpr (kEpi == ENC_FP8_OUT_FP8) {
+    // one block of 128 columns of a row per thread, held in registers: its scale needs all of them
+    float v[128];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      tmem_ld_32x32b_x32(taddr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+    if (lane == 0) bulk_wait_read0();
+    tmem_wait_ld();
+    release();
+    __syncwarp();   // the previous store has read the staging tile
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 128; j += 4) {
+      const float4 b = bias4(p, n0 + j);
+      add2(v[j], v[j + 1], v[j], v[j + 1], b.x, b.y);
+      add2(v[j + 2], v[j + 3], v[j + 2], v[j + 3], b.z, b.w);
+      if (p.gelu) {
+        gelu_fast2(v[j], v[j + 1]);
+        gelu_fast2(v[j + 2], v[j + 3]);
+      }
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(v[j]), fabsf(v[j + 1]))), fmaxf(fabsf(v[j + 2]), fabsf(v[j + 3])));
+    }
+    uint32_t bits = __float_as_uint(top);   // fmaxf passes over NaN
+    if (bits >= 0x7F800000u) {              // an infinity in the row: the largest finite magnitude instead
+      bits = 0;
+#pragma unroll
+      for (int j = 0; j < 128; ++j) bits = max(bits, finite_abs_bits(v[j]));
+    }
+    const uint32_t byte = e8m0_of_amax(bits);
+    const float inv = e8m0_inverse(byte);
+    uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float* t = v + 16 * j;
+      row[j ^ (lane & 7)] = make_uint4(e4m3x4(t[0], t[1], t[2], t[3], inv), e4m3x4(t[4], t[5], t[6], t[7], inv),
+                                       e4m3x4(t[8], t[9], t[10], t[11], inv), e4m3x4(t[12], t[13], t[14], t[15], inv));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map_c, stage, n0, r0);
+      bulk_commit();
+    }
+    const int r = r0 + lane, g = n0 / kFp8Block;
+    if (r < p.M) {
+      uint8_t* s = p.out_scales + (int64_t)r * p.out_pitch + g;
+      *s = static_cast<uint8_t>(byte);
+      if (g + 1 == fp8_blocks(p.N))
+        for (int i = g + 1; i < p.out_pitch; ++i) *++s = 127;
+    }
+  } else {
+    constexpr int kChunk = kEpi == ENC_FP8_OUT_BF16 ? 64 : 32;   // 128 bytes of a row
+    const int nc = cols / kChunk;
+#pragma unroll 1
+    for (int i = 0; i < nc; ++i) {
+      const int c = (down ? nc - 1 - i : i) * kChunk;
+      if (n0 + c >= p.N) continue;
+      uint32_t v[kChunk];
+#pragma unroll
+      for (int j = 0; j < kChunk; j += 32)
+        tmem_ld_32x32b_x32(taddr + c + j, *reinterpret_cast<uint32_t(*)[32]>(&v[j]));
+      if (lane == 0) bulk_wait_read0();   // the previous store has read the staging tile
+      tmem_wait_ld();
+      if (i == 0) release();
+      __syncwarp();
+      uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        constexpr int kPer = kChunk / 8;   // columns per 16-byte piece
+        float t[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; k += 4) {
+          const float4 b = bias4(p, n0 + c + kPer * j + k);
+          const uint32_t* a = v + kPer * j + k;
+          add2(t[k], t[k + 1], __uint_as_float(a[0]), __uint_as_float(a[1]), b.x, b.y);
+          add2(t[k + 2], t[k + 3], __uint_as_float(a[2]), __uint_as_float(a[3]), b.z, b.w);
+        }
+        if constexpr (kEpi == ENC_FP8_OUT_BF16) {
+          if (p.gelu) {
+#pragma unroll
+            for (int k = 0; k < kPer; k += 2) gelu_fast2(t[k], t[k + 1]);
+          }
+          row[j ^ (lane & 7)] = make_uint4(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]), pack_bf16x2(t[4], t[5]),
+                                           pack_bf16x2(t[6], t[7]));
+        } else {
+          if (kEpi == ENC_FP8_OUT_FP32 && p.gelu) {   // fp32 keeps what the fast form would lose
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) t[k] = gelu_erf(t[k]);
+          }
+          row[j ^ (lane & 7)] = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
+                                           __float_as_uint(t[3]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kEpi == ENC_FP8_OUT_RESID) tma_reduce_add_2d(map_c, stage, n0 + c, r0);
+        else tma_store_2d(map_c, stage, n0 + c, r0);
+        bulk_commit();
+      }
+    }
+  }
+}
+
+template <int kEpi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ CUtensorMap map_c, const GemmFp8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sW = sA + kStages * kOperandBytes;
+  uint8_t* stage_c = sW + kStages * kOperandBytes;                    // 4 KB per epilogue warp
+  uint8_t* sS = stage_c + kEpiWarps * 4096;                           // scale slots
+  uint64_t* full = reinterpret_cast<uint64_t*>(sS + kScaleSlots * kScaleSlotBytes);   // used in the first CTA
+  uint64_t* empty = full + kStages;
+  uint64_t* sfull = empty + kStages;        // [2] scales of both CTAs written; used in the first CTA
+  uint64_t* sempty = sfull + kScaleSlots;   // [2] MMAs that read the slot are done
+  uint64_t* tfull = sempty + kScaleSlots;   // [2] accumulator complete
+  uint64_t* tempty = tfull + 2;             // shared columns read; used in the first CTA
+  uint64_t* drain = tempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int units = p.num_tiles + p.tail;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < kScaleSlots; ++s) { mbar_init(&sfull[s], 2); mbar_init(&sempty[s], 1); }
+    for (int a = 0; a < 2; ++a) mbar_init(&tfull[a], 1);
+    mbar_init(tempty, 2 * kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) { tma_prefetch_desc(&map_a); tma_prefetch_desc(&map_w); tma_prefetch_desc(&map_c); }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any remote arrive or transaction
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  volatile int* abort_v = abort_flag;
+
+  // producer lane: bit s of `armed` = ring slot s received a load, whose phase parity is bit s of armed_phase
+  uint32_t armed = 0, armed_phase = 0;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = cluster; ok && u < units; u += nclusters) {
+        const Unit t = unit_at(p, u);
+        const int m0 = t.m0 + 128 * static_cast<int>(rank);
+        // a 128-wide unit uses the first 64 rows of each CTA's box (the rest is loaded and unused)
+        const int n0 = t.n0 + (t.width / 2) * static_cast<int>(rank);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+          if (leader) mbar_arrive_expect_tx(&full[stage], 4 * kOperandBytes);
+          const uint32_t bar = peer_addr(&full[stage], 0);
+          tma_load_2d_pair(sA + stage * kOperandBytes, &map_a, bar, kb * kBK, m0);
+          tma_load_2d_pair(sW + stage * kOperandBytes, &map_w, bar, kb * kBK, n0);
+          armed |= 1u << stage;
+          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        set_status(p.status, kDevTimeout);
+        *abort_v = 1;
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    // first CTA only: the whole warp walks the schedule, one elected lane issues
+    if (leader) {
+      const uint64_t adesc0 = smem_desc_sw128(smem_u32(sA)), wdesc0 = smem_desc_sw128(smem_u32(sW));
+      int stage = 0, slot = 0, acc = 0;
+      uint32_t phase = 0, sphase = 0, tphase = 0;
+      bool ok = true, issued = false;
+      for (int u = cluster; ok && u < units; u += nclusters) {
+        const uint32_t idesc = unit_at(p, u).width == 256 ? idesc_mxf8(256, 256) : idesc_mxf8(256, 128);
+        // the tile before: its columns shared with this one's accumulator have been read
+        if (!mbar_wait_warp(tempty, tphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+        tphase ^= 1u;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (acc ? kAcc1 : 0u);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          const uint32_t id = kb & 3;
+          const uint32_t sfa = tmem_base + kScaleCol + slot * kScaleSlotCols, sfb = sfa + 4;
+          if (id == 0 && !mbar_wait_warp(&sfull[slot], sphase, abort_v, kWaitLimitNs)) { ok = false; break; }
+          if (!mbar_wait_warp(&full[stage], phase, abort_v, kWaitLimitNs)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
+          const uint64_t wdesc = wdesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
+          const bool last = id == 3 || kb + 1 == p.num_kb;
+          if (elect_one()) {
+            if (id == 0) {
+              const uint64_t sdesc = smem_desc_scales(smem_u32(sS + slot * kScaleSlotBytes));
+#pragma unroll
+              for (int c = 0; c < 3; ++c) tmem_cp_scales_pair(sfa + 4 * c, sdesc + c * (512 >> 4));
+            }
+#pragma unroll
+            for (int k = 0; k < kBK / 32; ++k)   // +32 bytes along K inside the swizzled row
+              umma_mxf8_pair(d_tmem, adesc + static_cast<uint64_t>(2 * k), wdesc + static_cast<uint64_t>(2 * k),
+                             idesc | idesc_scale_id(id), sfa, sfb, (kb | k) != 0 ? 1u : 0u);
+            umma_commit_pair(&empty[stage], 0x3);
+            if (last) umma_commit_pair(&sempty[slot], 0x3);
+          }
+          __syncwarp();
+          issued = true;
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          if (last && ++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
+        __syncwarp();
+        acc ^= 1;
+      }
+      if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
+      if (issued) {   // every MMA done before the pair's TMEM and shared memory go away
+        if (elect_one()) umma_commit_pair(drain, 0x1);
+        __syncwarp();
+        mbar_wait_warp(drain, 0, nullptr, kWaitLimitNs);
+      }
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- scales
+    // Both CTAs: this CTA's 128 rows of A, all the unit's rows of W. The words of the next
+    // four blocks are loaded before the slot for them is free.
+    const uint32_t sfull_leader[kScaleSlots] = {peer_addr(&sfull[0], 0), peer_addr(&sfull[1], 0)};
+    int slot = 0;
+    uint32_t sphase = 0;
+    bool ok = true;
+    const int groups = (p.num_kb + 3) / 4;
+    for (int u = cluster; ok && u < units; u += nclusters) {
+      const Unit t = unit_at(p, u);
+      const int m0 = t.m0 + 128 * static_cast<int>(rank);
+      for (int g = 0; g < groups; ++g) {
+        uint32_t w[12];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = scale_word(p.a_scales, p.k_pitch, m0 + 32 * c + lane, p.M, g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          w[4 + c] = c * 32 < t.width ? scale_word(p.w_scales, p.k_pitch, t.n0 + 32 * c + lane, p.N, g) : kUnitScale;
+        if (!mbar_wait_warp(&sempty[slot], sphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+        uint4* dst = reinterpret_cast<uint4*>(sS + slot * kScaleSlotBytes) + lane;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) dst[c * 32] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();   // tcgen05.cp reads them through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(sfull_leader[slot]);
+        if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;                 // TMEM lanes this warp may read
+    const int half = (warp - kEpiWarp0) >> 2;     // which half of the unit's columns
+    uint8_t* stage = stage_c + (warp - kEpiWarp0) * 4096;
+    const uint32_t tempty_leader = peer_addr(tempty, 0);
+    int acc = 0;
+    uint32_t tphase = 0;
+    for (int u = cluster; u < units; u += nclusters) {
+      const Unit t = unit_at(p, u);
+      const int r0 = t.m0 + 128 * static_cast<int>(rank) + quarter * 32;
+      if (!mbar_wait(&tfull[acc], tphase, abort_v, kWaitLimitNs)) {
+        set_status(p.status, kDevTimeout);
+        *abort_v = 1;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      bool released = false;
+      auto release = [&]() {
+        if (released) return;
+        released = true;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_leader);
+      };
+      // e4m3 output: a row's block of 128 columns is one thread's, so a narrow unit is the first half's alone
+      const int per = kEpi == ENC_FP8_OUT_FP8 ? 128 : t.width / 2;
+      const int c0 = half * per, n0 = t.n0 + c0;
+      // the first accumulator's last columns are the second one's first
+      const bool shares = acc ? half == 0 : (half == 1 && t.width == 256);
+      if (!shares) release();
+      if (c0 < t.width && n0 < p.N && r0 < p.M) {
+        const uint32_t taddr =
+            tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(c0);
+        epilogue<kEpi>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, lane, release);
+      }
+      release();
+      acc ^= 1;
+      if (acc == 0) tphase ^= 1u;
+    }
+    if (lane == 0) bulk_wait0();   // the bulk stores / reduces have landed
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && lane == 0 && leader && *abort_v) {
+    // the first CTA's stage barriers count both CTAs' copies: after a failure, let
+    // every copy issued into the pair's rings land before either CTA leaves
+    for (int s = 0; s < kStages; ++s)
+      if (armed & (1u << s)) mbar_wait(&full[s], (armed_phase >> s) & 1u, nullptr, kWaitLimitNs / 4);
+  }
+  cluster_sync();   // no CTA leaves while its pair may still read its memory
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+template <int kEpi>
+cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cudaStream_t stream) {
+  static DeviceOnce once;
+  static int max_clusters[64] = {};   // written under once's mutex, read after its acquire
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidValue;
+  cudaError_t setup_error = cudaSuccess;
+  const bool ready = once.run(dev, [&] {
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_kernel<kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemBytes);
+    if (e != cudaSuccess) {
+      setup_error = e;
+      return false;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sm_count / 2), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_kernel<kEpi>, &cfg);
+    if (e != cudaSuccess || n < 1) n = sm_count / 2;   // every SM pairs up
+    cudaGetLastError();
+    if (n < 1) {
+      setup_error = cudaErrorInvalidValue;
+      return false;
+    }
+    max_clusters[dev & 63] = n;
+    return true;
+  });
+  if (!ready) return setup_error != cudaSuccess ? setup_error : cudaErrorInvalidValue;
+  const int ncl = max_clusters[dev & 63];
+  p.tiles_n = (p.N + 255) / 256;
+  p.num_tiles = ((p.M + 255) / 256) * p.tiles_n;
+  // a last wave that would run at most half full runs as two 128-wide halves per tile
+  // (not where the last column tile is narrow already)
+  const int tail = p.num_tiles % ncl;
+  const bool narrow = p.N - (p.tiles_n - 1) * 256 <= 128;
+  p.tail = (!narrow && 2 * tail <= ncl) ? tail : 0;
+  const int units = p.num_tiles + p.tail;
+  const int clusters = units < ncl ? units : ncl;
+  gemm_fp8_kernel<kEpi><<<2 * clusters, kThreads, kSmemBytes, stream>>>(m.a, m.w, m.c, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const GemmFp8Maps& m, const GemmFp8Params& p, int out_kind, int sm_count,
+                            cudaStream_t stream) {
+  if (p.M <= 0) return cudaSuccess;
+  switch (out_kind) {
+    case ENC_FP8_OUT_BF16: return launch_pair<ENC_FP8_OUT_BF16>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_FP32: return launch_pair<ENC_FP8_OUT_FP32>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_FP8: return launch_pair<ENC_FP8_OUT_FP8>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_RESID: return launch_pair<ENC_FP8_OUT_RESID>(m, p, sm_count, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace enc

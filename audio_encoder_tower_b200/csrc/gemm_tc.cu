@@ -69,23 +69,6 @@ __device__ __forceinline__ void a_coords(const GemmTcParams& p, int m0, int kb, 
   }
 }
 
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// resid[y .. y+32, x .. x+32) += the 32x32 fp32 tile at smem (tensor-map layout,
-// 128-byte swizzle), reduced in L2 by the TMA unit; rows past the map's end are
-// skipped. Completion is tracked with bulk groups.
-__device__ __forceinline__ void tma_reduce_add_2d(const void* map, const void* smem, int x, int y) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem)), "r"(x), "r"(y)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // x[r0 .. r0+32, n0 .. n0+32*NC) += acc + bias for the warp's 32 accumulator rows.
 // Each 32-column chunk goes through the warp's 4 KB staging tile: thread = row
 // writes its 32 values (16-byte pieces XOR-swizzled by row, as the tensor map's
@@ -118,15 +101,6 @@ __device__ __forceinline__ void epi_residual_tile(const EpiParams& e, const CUte
       bulk_commit();
     }
   }
-}
-
-// out[y .. y+32, x .. x+64) = the 32x64 bf16 tile at smem (tensor-map layout,
-// 128-byte swizzle); rows past the map's end are skipped.
-__device__ __forceinline__ void tma_store_2d(const void* map, const void* smem, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem)), "r"(x), "r"(y)
-               : "memory");
 }
 
 // out[r0 .. r0+32, n0 .. n0+64*NC) = act(acc + bias) as bf16 for the warp's 32
@@ -185,33 +159,6 @@ __device__ __forceinline__ void epi_store_tile(const EpiParams& e, const CUtenso
 }
 
 // ------------------------------------------------------ pairs of CTAs (2-SM MMA)
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// shared::cluster address of the same shared variable in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// TMA load into this CTA's shared memory whose transaction bytes count on the
-// barrier of the pair's first CTA (the one that issues the MMAs). Not a
-// multicast: every CTA loads only its own operand halves.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uint32_t bar_cluster, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-      "%4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
-      : "memory");
-}
 // D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, M = 256 over the pair.
 __device__ __forceinline__ void umma_f16_ss_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                  uint32_t accumulate) {
@@ -222,15 +169,6 @@ __device__ __forceinline__ void umma_f16_ss_pair(uint32_t d_tmem, uint64_t adesc
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrive on `bar` in every CTA of `mask` once the pair's previously issued MMAs are done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
-}
-
 // Epilogue instantiations: each keeps the whole register budget to itself.
 enum EpiKind : int {
   EK_GENERIC = 0,   // per-thread stores (conv2 scatter + position table, projector scatter)
@@ -795,6 +733,33 @@ bool make_tma_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64_
   cuuint32_t box[2] = {32, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_fp8_operand_map(CUtensorMap* map, const void* q, int rows, int cols) {
+  auto fn = encode_fn();
+  if (!fn || !q || (reinterpret_cast<uintptr_t>(q) & 15u) || (cols & 15)) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols};
+  cuuint32_t box[2] = {128, 128};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_fp8_out_map(CUtensorMap* map, const void* out, int out_kind, int rows, int cols) {
+  if (out_kind == ENC_FP8_OUT_BF16) return make_out_map(map, out, (uint64_t)rows, (uint64_t)cols);
+  if (out_kind != ENC_FP8_OUT_FP8)
+    return make_resid_map(map, reinterpret_cast<const float*>(out), (uint64_t)rows, (uint64_t)cols);
+  auto fn = encode_fn();
+  if (!fn || !out || (reinterpret_cast<uintptr_t>(out) & 15u) || (cols & 15)) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols};
+  cuuint32_t box[2] = {128, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(out), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

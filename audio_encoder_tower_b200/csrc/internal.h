@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "../../include/enc.h"
+#include "../../include/enc_fp8.h"
 
 namespace enc {
 
@@ -98,6 +99,34 @@ bool make_resid_map(CUtensorMap* map, const float* resid, uint64_t rows, uint64_
 // optional bf16 output map from make_out_map (TMA-store epilogue when given).
 cudaError_t launch_gemm_tc(const CUtensorMap& map_a, const CUtensorMap& map_b, GemmTcParams p, int sm_count,
                            cudaStream_t stream, const CUtensorMap* map_c = nullptr);
+
+// ------------------------------------------------------- 8-bit (e4m3) operators
+struct GemmFp8Params {
+  int M, N, num_kb;         // output rows / columns; K / 128 rounded up
+  int tiles_n, num_tiles;   // filled by the launcher
+  int tail;                 // the last `tail` tiles run as two 256 x 128 halves (launcher)
+  const uint8_t *a_scales, *w_scales;
+  int k_pitch;              // bytes per row of a_scales and w_scales
+  const float* bias;        // [N] or nullptr
+  int gelu;
+  uint8_t* out_scales;      // ENC_FP8_OUT_FP8
+  int out_pitch;
+  int* status;
+};
+// Operands (128 x 128 byte boxes) and output (32 rows x 128 bytes), 128-byte swizzle.
+struct GemmFp8Maps {
+  CUtensorMap a, w, c;
+};
+// e4m3 [rows, cols] operand; out_kind's [rows, cols] output.
+bool make_fp8_operand_map(CUtensorMap* map, const void* q, int rows, int cols);
+bool make_fp8_out_map(CUtensorMap* map, const void* out, int out_kind, int rows, int cols);
+cudaError_t launch_gemm_fp8(const GemmFp8Maps& m, const GemmFp8Params& p, int out_kind, int sm_count,
+                            cudaStream_t stream);
+cudaError_t launch_quantize_fp8(const void* x, bool x_bf16, int64_t ldx, int rows, int cols, uint8_t* q,
+                                uint8_t* scales, cudaStream_t s);
+cudaError_t launch_norm_fp8(int kind, const void* x, bool x_bf16, int64_t ldx, const void* delta, bool delta_bf16,
+                            int64_t ldd, const float* gamma, const float* beta, float eps, int rows, int d,
+                            void* x_out, int64_t ldxo, uint8_t* q, uint8_t* scales, cudaStream_t s);
 
 // --------------------------------------------------------- fp32 check path
 // C = A[M, K] (row stride lda, rows may overlap) * W[N, K]^T (row stride ldw).

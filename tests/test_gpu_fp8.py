@@ -1,0 +1,412 @@
+"""The 8-bit operators on the GPU against the float64 oracle (oracle/fp8.py):
+quantisation bit for bit, the norm and the matrix product within what their fp32
+arithmetic and the final rounding can be off by."""
+import math
+
+import numpy as np
+import pytest
+
+import oracle.fp8 as F8
+
+pytestmark = pytest.mark.gpu
+
+E32 = 2.0 ** -24          # fp32: half a step, relative
+HALF = {"bf16": 2.0 ** -8, "fp8": 2.0 ** -4, "fp32": 2.0 ** -24}
+
+
+def _t(a, dtype=None):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).to(device="cuda", dtype=dtype or torch.float32)
+
+
+def _deq(q, scales):
+    """(float64 values, exponents) of a device matrix in the 8-bit format; checks the padding bytes."""
+    import torch
+    nb = -(-q.shape[1] // 128)
+    by = scales.view(torch.uint8).cpu().numpy().astype(np.int64)
+    assert np.all(by[:, nb:] == 127)
+    e = by[:, :nb] - 127
+    return q.cpu().to(torch.float64).numpy() * F8.spread(e, q.shape[1]), e
+
+
+def _rows(rng, rows, cols):
+    """Rows whose blocks differ in size by up to 2^60, with zero rows and zero blocks."""
+    x = rng.standard_normal((rows, cols)) * F8.spread(rng.integers(-30, 31, (rows, -(-cols // 128))), cols)
+    if rows > 2:
+        x[1] = 0
+        x[2, :min(cols, 128)] = 0
+    return x.astype(np.float32)
+
+
+# -------------------------------------------------------------------- quantise
+@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 128), (2, 144), (5, 512), (7, 1040), (33, 1280), (4, 1168),
+                                       (2, 4096), (1, 65536)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_quantize(rows, cols, dtype):
+    import torch
+    from audio_encoder_tower_b200 import quantize_fp8
+    x = _t(_rows(np.random.default_rng(rows * cols), rows, cols), torch.bfloat16 if dtype == "bf16" else None)
+    q, s = quantize_fp8(x)
+    got, e = _deq(q, s)
+    want, we = F8.quantize(x.double().cpu().numpy())
+    assert np.array_equal(e, we)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_quantize_special_values(dtype):
+    """Borders of the scale, the largest and smallest magnitudes, NaN and infinities beside finite values."""
+    import torch
+    from audio_encoder_tower_b200 import quantize_fp8
+    tiny = 2.0 ** -126
+    rows = [[448.0], [450.0], [-1.75, 1.0, 0.01], [3.3e38, 1.0, 1e30], [tiny, -tiny / 2], [2.0 ** -133],
+            [np.inf, 3.0, -1.0], [-np.inf, np.nan, 1e-3], [np.nan], [0.0, -0.0], [1e-30, -1e-36, 1e-38]]
+    x = np.zeros((len(rows), 272))
+    for i, r in enumerate(rows):
+        x[i, 7:7 + len(r)] = r
+        x[i, 200], x[i, 271] = 5.0, -448.0      # the other blocks are not affected
+    x = _t(x.astype(np.float32), torch.bfloat16 if dtype == "bf16" else None)
+    q, s = quantize_fp8(x)
+    got, e = _deq(q, s)
+    want, we = F8.quantize(x.double().cpu().numpy())
+    assert np.array_equal(e, we)
+    assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_quantize_strides_and_neighbours():
+    """Rows inside a wider matrix; rows of the outputs past the last one stay as they were."""
+    import torch
+    from audio_encoder_tower_b200 import quantize_fp8
+    x = _t(_rows(np.random.default_rng(3), 9, 2000), torch.bfloat16)
+    part = x[:, 8:8 + 656]
+    q = torch.full((12, 656), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((12, 8), 0x55, dtype=torch.uint8, device="cuda")
+    quantize_fp8(part, q=q[:9].view(torch.float8_e4m3fn), scales=s[:9])
+    got, e = _deq(q[:9].view(torch.float8_e4m3fn), s[:9])
+    want, we = F8.quantize(part.double().cpu().numpy())
+    assert np.array_equal(e, we) and np.array_equal(got, want)
+    assert bool((q[9:] == 0x55).all()) and bool((s[9:] == 0x55).all())
+
+
+def test_quantize_past_32_bits():
+    """More elements than 2^31: the last rows are where their offsets say."""
+    import torch
+    from audio_encoder_tower_b200 import quantize_fp8
+    rows, cols = 1_700_000, 1280
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = _t(_rows(np.random.default_rng(5), 3, cols), torch.bfloat16)
+    q, s = quantize_fp8(x)
+    got, e = _deq(q[-3:], s[-3:])
+    want, we = F8.quantize(x[-3:].double().cpu().numpy())
+    assert np.array_equal(e, we) and np.array_equal(got, want)
+    assert int(q[:-3].view(torch.uint8).max()) == 0
+
+
+# ------------------------------------------------------------------------ norm
+def _check_norm(got, e, y, slack):
+    """Each value is within half an e4m3 step of some value within `slack` of y, and each
+    scale is the least for an amax within `slack` of y's."""
+    lo, hi = np.abs(y) - slack, np.abs(y) + slack
+    elo, ehi = F8.exponents(np.maximum(lo, 0)), F8.exponents(hi)
+    assert np.all((e >= elo) & (e <= ehi))
+    step = np.maximum(HALF["fp8"] * hi, 2.0 ** -10 * F8.spread(e, y.shape[1]))   # subnormal step 2^-9
+    assert np.all(np.abs(got - y) <= step + slack)
+
+
+@pytest.mark.parametrize("rows,d", [(1, 16), (1, 1280), (9, 128), (5, 144), (17, 384), (8, 656), (3, 1024), (33, 1280),
+                                    (6, 1536), (2, 2048), (5, 2064), (3, 4016), (2, 4112), (2, 8192)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("x_type,delta_type", [("bf16", "bf16"), ("fp32", "bf16"), ("fp32", None), ("bf16", "fp32")])
+def test_norm(rows, d, kind, x_type, delta_type):
+    import torch
+    from audio_encoder_tower_b200 import norm_fp8
+    T = {"bf16": torch.bfloat16, "fp32": torch.float32}
+    rng = np.random.default_rng(rows * 10000 + d)
+    x = _t((rng.standard_normal((rows, d)) * 3 + 0.5).astype(np.float32), T[x_type])
+    delta = None if delta_type is None else _t(rng.standard_normal((rows, d)).astype(np.float32), T[delta_type])
+    gamma = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32)
+    beta = (0.1 * rng.standard_normal(d)).astype(np.float32) if kind == "layer" else None
+    before = x.clone()
+    q, s, xo = norm_fp8(x, _t(gamma), None if beta is None else _t(beta), delta=delta, kind=kind)
+    assert torch.equal(x, before)
+    want_x = x if delta is None else (x.float() + delta.float()).to(x.dtype)
+    assert torch.equal(xo, want_x)                        # one fp32 addition and one rounding: exact
+    st = want_x.double().cpu().numpy()
+    y = F8.norm(st, gamma, beta, kind)
+    got, e = _deq(q, s)
+    # fp32: a sum of n terms in a tree of lanes and registers is off by at most (n / 32 / WPR + 7) * E32 <= 80 E32
+    # of the sum of magnitudes; half of that reaches the root, all of the mean's reaches x - mean; a handful of
+    # roundings per element on top
+    sd = np.sqrt(((st - (st.mean(1, keepdims=True) if kind == "layer" else 0)) ** 2).mean(1, keepdims=True) + 1e-5)
+    core = np.abs(st) / sd * np.abs(gamma)
+    slack = 60 * E32 * (core + (0 if beta is None else np.abs(beta)))
+    if kind == "layer":
+        slack = slack + 80 * E32 * np.abs(st).mean(1, keepdims=True) / sd * np.abs(gamma)
+    _check_norm(got, e, y, slack)
+
+
+def test_norm_in_place_strides_and_neighbours():
+    import torch
+    from audio_encoder_tower_b200 import norm_fp8
+    rng = np.random.default_rng(12)
+    wide = _t(rng.standard_normal((10, 1500)).astype(np.float32), torch.bfloat16)
+    dwide = _t(rng.standard_normal((7, 720)).astype(np.float32), torch.bfloat16)
+    x, delta = wide[:7, 16:16 + 704], dwide[:, 8:712]
+    gamma = _t(np.ones(704, np.float32))
+    want = wide.clone()
+    want[:7, 16:720] = (x.float() + delta.float()).to(torch.bfloat16)
+    q, s, xo = norm_fp8(x, gamma, delta=delta, x_out=x)
+    assert torch.equal(wide, want) and xo.data_ptr() == x.data_ptr()
+    y = F8.norm(x.double().cpu().numpy(), np.ones(704))
+    got, e = _deq(q, s)
+    _check_norm(got, e, y, 60 * E32 * np.abs(y))
+
+
+def test_norm_special_rows():
+    """A zero row stays zero; a NaN or an infinity makes its own row NaN and no other."""
+    import torch
+    from audio_encoder_tower_b200 import norm_fp8
+    rng = np.random.default_rng(13)
+    x = rng.standard_normal((6, 1280)).astype(np.float32)
+    x[1], x[2, 5], x[4, 1279] = 0, np.nan, np.inf
+    for kind in ("rms", "layer"):
+        q, s, _ = norm_fp8(_t(x), _t(np.ones(1280, np.float32)), kind=kind)
+        got, e = _deq(q, s)
+        assert np.all(got[1] == 0) and np.all(np.isfinite(got[[0, 1, 3, 5]]))
+        assert np.isnan(got[2]).all()
+        assert np.isnan(got[4, 1279])
+        y = F8.norm(x[[0, 3, 5]], np.ones(1280), None, kind)
+        _check_norm(got[[0, 3, 5]], e[[0, 3, 5]], y, 150 * E32 * (np.abs(y) + 1))
+
+
+# ---------------------------------------------------------------- matrix product
+def _operand(rng, rows, cols, spread=2, scale=1.0):
+    """A device matrix in the 8-bit format with exactly known values: (q, scales, float64 values)."""
+    from audio_encoder_tower_b200 import quantize_fp8
+    x = rng.standard_normal((rows, cols)) * scale
+    x = x * F8.spread(rng.integers(-spread, spread + 1, (rows, -(-cols // 128))), cols)
+    q, s = quantize_fp8(_t(x.astype(np.float32)))
+    return q, s, _deq(q, s)[0]
+
+
+def _acc_slack(a, w, K):
+    """What fp32 accumulation may be off by: each MMA of 32 products adds to the running sum
+    with an error of at most two steps (2^-22) of the magnitudes seen so far."""
+    return (K / 32 + 4) * 2.0 ** -22 * (np.abs(a) @ np.abs(w).T)
+
+
+SHAPES = [(1, 16, 16), (1, 128, 128), (1, 1280, 1280), (3, 272, 144), (16, 512, 1104), (50, 384, 1024), (64, 144, 640),
+          (100, 1360, 512), (127, 256, 656), (128, 400, 128), (129, 128, 2064), (200, 1280, 1280), (257, 640, 1280),
+          (300, 272, 1168), (513, 1296, 272), (1000, 512, 528), (4000, 3840, 1280)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("out", ["bf16", "fp32", "fp8", "resid"])
+def test_linear(M, N, K, out):
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(M * 7 + N * 3 + K)
+    a, sa, av = _operand(rng, M, K)
+    w, sw, wv = _operand(rng, N, K, scale=1 / math.sqrt(K))
+    bias = rng.standard_normal(N).astype(np.float32) if N != 512 else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gelu = out != "resid" and N % 256 == 0
+    slack = _acc_slack(av, wv, K)
+    y = F8.linear(av, wv, bias)
+    slack = slack + 2 * E32 * (np.abs(y) + np.abs(y - (0 if bias is None else bias)))
+    # GELU's slope is at most 1.13; the bf16 and e4m3 epilogues use a form within 1.1e-5 of it (relative),
+    # or 4.1e-11 |x| below -6.5; erff and its product a few steps of fp32
+    if gelu:
+        slack = 1.13 * slack + (8 * E32 if out == "fp32" else 1.3e-5) * np.abs(F8.linear(av, wv, bias, True)) + \
+            (8 * E32 if out == "fp32" else 5e-11) * np.abs(y)
+        y = F8.linear(av, wv, bias, True)
+    b = None if bias is None else _t(bias)
+    if out == "resid":
+        base = rng.standard_normal((M + 3, N)).astype(np.float32)
+        buf = _t(base)
+        r = linear_fp8(a, sa, w, sw, bias=b, resid=buf[:M], status=status)
+        assert r.data_ptr() == buf.data_ptr() and np.array_equal(buf[M:].cpu().numpy(), base[M:])
+        got = buf[:M].double().cpu().numpy()
+        y = y + base[:M]
+        assert np.all(np.abs(got - y) <= slack + 2 * E32 * (np.abs(y) + np.abs(base[:M])))
+    elif out == "fp8":
+        o = torch.full((M + 3, N), 0x55, dtype=torch.uint8, device="cuda")
+        s = torch.full((M + 3, sw.shape[1] if N == K else -(-N // 512) * 4), 0x55, dtype=torch.uint8, device="cuda")
+        q, so = linear_fp8(a, sa, w, sw, bias=b, out=o[:M].view(torch.float8_e4m3fn), out_scales=s[:M], gelu=gelu,
+                           status=status)
+        assert bool((o[M:] == 0x55).all()) and bool((s[M:] == 0x55).all())
+        got, e = _deq(q, so)
+        _check_norm(got, e, y, slack)
+    else:
+        T = torch.bfloat16 if out == "bf16" else torch.float32
+        o = torch.full((M + 3, N), 7.0, dtype=T, device="cuda")
+        linear_fp8(a, sa, w, sw, bias=b, out=o[:M], gelu=gelu, status=status)
+        assert bool((o[M:] == 7).all())
+        got = o[:M].double().cpu().numpy()
+        assert np.all(np.abs(got - y) <= slack + HALF[out] * (np.abs(y) + slack))
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 144, 640), (96, 272, 1168), (300, 512, 1280), (700, 1280, 528)])
+def test_linear_exact(M, N, K):
+    """Small whole numbers under powers of two that differ from block to block: every partial sum
+    is a number of fp32, so the result is the exact one in any order."""
+    from audio_encoder_tower_b200 import linear_fp8, quantize_fp8
+    rng = np.random.default_rng(K)
+    v = []
+    for rows in (M, N):
+        x = rng.integers(-4, 5, (rows, K)) * F8.spread(rng.integers(-2, 3, (rows, -(-K // 128))), K)
+        q, s = quantize_fp8(_t(x.astype(np.float32)))
+        assert np.array_equal(_deq(q, s)[0], x)
+        v.append((q, s, x))
+    (a, sa, av), (w, sw, wv) = v
+    got = linear_fp8(a, sa, w, sw, out_dtype="fp32").double().cpu().numpy()
+    assert np.array_equal(got, av @ wv.T)
+
+
+def test_linear_scales_far_apart():
+    """Block scales from 2^-60 to 2^60 on both sides, one block of each row far above the rest."""
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(21)
+    for M, N, K in ((40, 256, 1280), (400, 256, 1280)):
+        a, sa, av = _operand(rng, M, K, spread=30)
+        w, sw, wv = _operand(rng, N, K, spread=30)
+        got = linear_fp8(a, sa, w, sw, out_dtype="fp32").double().cpu().numpy()
+        assert np.all(np.abs(got - av @ wv.T) <= _acc_slack(av, wv, K))
+
+
+def test_linear_nan_stays_in_its_row():
+    """A NaN element, or a NaN scale (byte 255), makes its row of A and its row of W NaN and nothing else."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(22)
+    for M in (20, 300):
+        a, sa, av = _operand(rng, M, 656)
+        w, sw, wv = _operand(rng, 272, 656)
+        a.view(torch.uint8)[3, 100] = 0x7F
+        sa.view(torch.uint8)[7, 5] = 255
+        w.view(torch.uint8)[271, 655] = 0xFF
+        got = linear_fp8(a, sa, w, sw, out_dtype="fp32").double().cpu().numpy()
+        nan = np.zeros((M, 272), bool)
+        nan[3], nan[7], nan[:, 271] = True, True, True
+        assert np.array_equal(np.isnan(got), nan)
+        ok = ~nan
+        assert np.all(np.abs(got - av @ wv.T)[ok] <= _acc_slack(av, wv, 656)[ok])
+        # the same blocks in e4m3: NaN elements, the rest of the block as without them
+        q, s = linear_fp8(a, sa, w, sw, out_dtype="fp8")
+        got8, _ = _deq(q, s)
+        assert np.array_equal(np.isnan(got8), nan)
+
+
+def test_linear_row_does_not_depend_on_its_neighbours():
+    """The same row, alone and among others, within a tile and in another one, gives the same bits per kernel
+    variant, and the same call twice gives the same bits."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(23)
+    a, sa, _ = _operand(rng, 900, 1280)
+    w, sw, _ = _operand(rng, 512, 1280)
+    full = linear_fp8(a, sa, w, sw, out_dtype="fp32")
+    assert torch.equal(full, linear_fp8(a, sa, w, sw, out_dtype="fp32"))
+    perm = torch.randperm(900, device="cuda")
+    part = linear_fp8(a.view(torch.uint8)[perm].view(a.dtype), sa.view(torch.uint8)[perm].view(sa.dtype), w, sw,
+                      out_dtype="fp32")
+    assert torch.equal(part, full[perm])
+
+
+def test_no_rows():
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8, norm_fp8, quantize_fp8
+    x = torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda")
+    q, s = quantize_fp8(x)
+    q2, s2, xo = norm_fp8(x, torch.ones(256, device="cuda"), delta=x)
+    w, sw, _ = _operand(np.random.default_rng(1), 32, 256)
+    assert linear_fp8(q, s, w, sw).shape == (0, 32) and q2.shape == (0, 256) and xo.shape == (0, 256)
+
+
+# ------------------------------------------------------- together, streams, graphs
+def _ffn(x, gamma, beta, w1, w2, resid, stream=None):
+    """LayerNorm -> fc1 + GELU (e4m3 out) -> fc2 added to the stream: a block's feed-forward half."""
+    from audio_encoder_tower_b200 import linear_fp8, norm_fp8
+    q, s, _ = norm_fp8(x, gamma, beta, kind="layer", stream=stream)
+    h, hs = linear_fp8(q, s, w1[0], w1[1], bias=w1[2], out_dtype="fp8", gelu=True, stream=stream)
+    return linear_fp8(h, hs, w2[0], w2[1], bias=w2[2], resid=resid, stream=stream)
+
+
+def _ffn_case(seed, rows, d=640, f=1296):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((rows, d)).astype(np.float32)
+    g, b = (1 + 0.1 * rng.standard_normal(d)).astype(np.float32), (0.1 * rng.standard_normal(d)).astype(np.float32)
+    w1 = _operand(rng, f, d, scale=1 / math.sqrt(d), spread=0)
+    w2 = _operand(rng, d, f, scale=1 / math.sqrt(f), spread=0)
+    b1, b2 = (0.1 * rng.standard_normal(n).astype(np.float32) for n in (f, d))
+    return x, g, b, w1, w2, b1, b2
+
+
+@pytest.mark.parametrize("rows", [1, 50, 333])
+def test_feed_forward_chain(rows):
+    """norm -> product with GELU -> product onto the stream, against the float64 formulas with the
+    8-bit roundings in the same places. A value near the middle between two e4m3 values may fall on
+    either side, so the result may differ by a few of those steps: compared in norm with the error
+    that the roundings themselves cause."""
+    import torch
+    x, g, b, w1, w2, b1, b2 = _ffn_case(31, rows)
+    xt = _t(x)
+    _ffn(xt, _t(g), _t(b), (*w1[:2], _t(b1)), (*w2[:2], _t(b2)), xt)
+    torch.cuda.synchronize()
+    got = xt.double().cpu().numpy()
+    y = F8.norm(x, g, b, "layer")
+    exact = x + F8.linear(F8.linear(y, w1[2], b1, True), w2[2], b2)
+    h, _ = F8.quantize(F8.linear(F8.quantize(y)[0], w1[2], b1, True))
+    model = x + F8.linear(h, w2[2], b2)
+    noise = np.linalg.norm(model - exact)
+    assert np.linalg.norm(got - model) <= 0.1 * noise, (np.linalg.norm(got - model), noise)
+
+
+def test_captured_and_replayed():
+    """The chain captured into a graph and replayed on new data gives the eager call's bits."""
+    import torch
+    x, g, b, w1, w2, b1, b2 = _ffn_case(32, 70)
+    dev = [_t(v) for v in (g, b, b1, b2)]
+    args = (dev[0], dev[1], (*w1[:2], dev[2]), (*w2[:2], dev[3]))
+    want = []
+    for k in (1, 2):
+        r = _t(x * k)
+        want.append(_ffn(r.clone(), *args, resid=r).clone())
+    buf, res = _t(x), _t(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _ffn(buf, *args, resid=res)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _ffn(buf, *args, resid=res)
+    for k in (1, 2):
+        buf.copy_(_t(x * k))
+        res.copy_(buf)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res, want[k - 1])
+
+
+def test_two_streams_at_once():
+    """Independent chains on two streams, started together, give what each gives alone."""
+    import torch
+    cases = []
+    for seed in (33, 34):
+        x, g, b, w1, w2, b1, b2 = _ffn_case(seed, 600)
+        cases.append((_t(x), _t(g), _t(b), (*w1[:2], _t(b1)), (*w2[:2], _t(b2))))
+    alone = [_ffn(*c, resid=c[0].clone()).clone() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    out = [c[0].clone() for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                out[i].copy_(c[0])
+            _ffn(*c, resid=out[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(out[i], alone[i])
