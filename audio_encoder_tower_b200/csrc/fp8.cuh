@@ -28,17 +28,13 @@ __device__ __forceinline__ uint32_t finite_abs_bits(float v) {
   return b < 0x7F800000u ? b : 0u;
 }
 
-// Two values / 2^e as e4m3 (low byte: a). |value / 2^e| <= 448 where it is finite; an
-// infinity turns into NaN by the product with zero, and e4m3 keeps NaN.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b, float inv) {
-  a = fmaf(a, 0.f, a * inv);
-  b = fmaf(b, 0.f, b * inv);
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv) {
-  return e4m3x2(a, b, inv) | (e4m3x2(c, d, inv) << 16);
+// Four values, already divided by their scale, as e4m3 (low byte first). Finite values are at
+// most 448 in magnitude; e4m3 keeps NaN, and an infinity has been turned into NaN before.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
 }  // namespace enc

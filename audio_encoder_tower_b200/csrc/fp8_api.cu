@@ -50,7 +50,7 @@ int32_t enc_fp8_scale_pitch(int32_t cols) { return cols < 1 ? 0 : (int32_t)(((in
 enc_status enc_quantize_fp8(const void* x, int32_t x_dtype, int64_t ldx, int32_t rows, int32_t cols, void* q,
                             void* scales, cudaStream_t stream) {
   if (!dtype_ok(x_dtype) || rows < 0 || cols <= 0) return ENC_ERR_INVALID_ARG;
-  if (cols % 16 || cols > 65536) return ENC_ERR_UNSUPPORTED;
+  if (cols % 16 || cols > 65536 || (int64_t)rows * fp8_blocks(cols) >= (1ll << 31) - 4096) return ENC_ERR_UNSUPPORTED;
   if (rows == 0) return ENC_OK;
   if (!x || !q || !scales || !rows_ok(x, ldx, cols) || !aligned(q, 16) || !aligned(scales, 4))
     return ENC_ERR_INVALID_ARG;

@@ -139,16 +139,21 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
     if (bits >= 0x7F800000u) {              // an infinity in the row: the largest finite magnitude instead
       bits = 0;
 #pragma unroll
-      for (int j = 0; j < 128; ++j) bits = max(bits, finite_abs_bits(v[j]));
+      for (int j = 0; j < 128; ++j) {
+        bits = max(bits, finite_abs_bits(v[j]));
+        v[j] = fmaf(v[j], 0.f, v[j]);       // and the infinity turns into NaN
+      }
     }
     const uint32_t byte = e8m0_of_amax(bits);
     const float inv = e8m0_inverse(byte);
     uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float* t = v + 16 * j;
-      row[j ^ (lane & 7)] = make_uint4(e4m3x4(t[0], t[1], t[2], t[3], inv), e4m3x4(t[4], t[5], t[6], t[7], inv),
-                                       e4m3x4(t[8], t[9], t[10], t[11], inv), e4m3x4(t[12], t[13], t[14], t[15], inv));
+      float t[16];
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) mul2(t[k], t[k + 1], v[16 * j + k], v[16 * j + k + 1], inv, inv);
+      row[j ^ (lane & 7)] = make_uint4(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]),
+                                       e4m3x4(t[8], t[9], t[10], t[11]), e4m3x4(t[12], t[13], t[14], t[15]));
     }
     fence_proxy_async_smem();
     __syncwarp();

@@ -43,7 +43,7 @@ ENC_API int32_t enc_fp8_scale_pitch(int32_t cols);
  * Rows to e4m3 with block scales.
  *   x       [rows, cols] of x_dtype (enc_dtype), row stride ldx elements (>= cols);
  *           16-byte aligned, ldx a multiple of 4
- *   cols    a multiple of 16, <= 65536
+ *   cols    a multiple of 16, <= 65536; rows * ceil(cols / 128) below 2^31 - 4096
  */
 ENC_API enc_status enc_quantize_fp8(const void *x, int32_t x_dtype, int64_t ldx, int32_t rows, int32_t cols,
                                     void *q, void *scales, cudaStream_t stream);
