@@ -464,6 +464,12 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without release semantics: for a thread whose reads of TMEM (ordered by
+// tc_fence_before) are all that the waiting thread must come after. The releasing form first
+// waits for the thread's earlier memory operations.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // TMA load into this CTA's shared memory whose transaction bytes count on the
 // barrier of the pair's first CTA (the one that issues the MMAs). Not a
 // multicast: every CTA loads only its own operand halves.

@@ -64,22 +64,25 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
 // --------------------------------------------------------------- shape of the kernel
 // A cluster of two CTAs computes 256 x 256 tiles (M = 256 over the pair). CTA r holds
 // rows 128 r .. of the A tile and rows 128 r .. of the W tile in a ring of 32 KB stages.
-//   warp 0   TMA producer;  warp 1 (first CTA)  MMA issuer;  warp 2  scales
-//   warps 3..10  epilogue: warps of a TMEM lane quarter split the tile's columns
+//   warp 0   TMA producer;  warp 2  scales;  warp 3  none
+//   warp 1   first CTA: MMA issuer; second CTA: tells the first that its scales are written
+//   warps 4..  epilogue: warps of a TMEM lane quarter split the tile's columns
 // TMEM has 512 columns: two accumulators of 256 and the scales do not fit side by side.
 // The accumulators overlap instead, by 32 columns: 0..255 and 224..479, scales from
 // 480. A tile's MMAs may start once the epilogue has read the 32 shared columns of the
 // tile before, which it therefore reads first; the rest of its work still overlaps the
 // next tile's MMAs.
-constexpr int kEpiWarp0 = 3, kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kEpiWarp0 = 4;
 constexpr int kStages = 5;
 constexpr uint32_t kOperandBytes = 128 * kBK;          // per stage: this CTA's 128 rows of A, and of W
 constexpr uint32_t kTmemCols = 512, kAcc1 = 224, kScaleCol = 480, kScaleSlotCols = 12;
 constexpr uint32_t kScaleSlotBytes = 3 * 512;          // A: 128 rows, W: 256 rows
-constexpr int kScaleSlots = 2;
-constexpr size_t kSmemBytes = 1024 + kStages * (size_t)(2 * kOperandBytes) + kEpiWarps * (size_t)4096 +
-                              kScaleSlots * kScaleSlotBytes + 512;
+constexpr int kScaleSlots = 4, kScaleTmemSlots = 2;    // in shared memory, in TMEM
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr size_t kSmemBytes = 1024 + kStages * (size_t)(2 * kOperandBytes) + kEpiWarps * 4096 /*staging*/ +
+                              kScaleSlots * kScaleSlotBytes + kEpiWarps * 512 /*bias*/ + 512;
 
 // Work units: tiles of 256 x 256 in row-major order, the last `tail` of them as two
 // halves of 128 columns, so that a last wave under half full keeps more SMs busy. A last
@@ -102,40 +105,72 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int pitch, int 
   return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(s + (int64_t)row * pitch) + g) : kUnitScale;
 }
 
-__device__ __forceinline__ float4 bias4(const GemmFp8Params& p, int c) {
-  if (p.bias && c < p.N) return __ldg(reinterpret_cast<const float4*>(p.bias + c));   // N is a multiple of 16
-  return make_float4(0.f, 0.f, 0.f, 0.f);
+// Four values from the warp's copy of the bias (all lanes the same address: a broadcast).
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// GELU for an e4m3 result, on packed pairs: max(x, 0) - |x| 2^G(|x|) as gelu_fast2, with
+// G = log2 Phi(-a) from a minimax polynomial of degree 5 over [0, 5.5] (relative error of the
+// result there at most 2.5e-4, a 250th of half an e4m3 step). Beyond, the polynomial keeps
+// falling, so no clamp is needed: the result is within 1.9e-8 |x| of max(x, 0), as GELU is.
+__device__ __forceinline__ void gelu_e4m3_2(float& x0, float& x1) {
+  constexpr float c0 = -1.000359058380127f, c1 = -1.1462607383728027f, c2 = -0.4696812331676483f,
+                  c3 = -0.04459895193576813f, c4 = 0.004869762342423201f, c5 = -0.00023325053916778415f;
+  const float a0 = fabsf(x0), a1 = fabsf(x1);
+  float g0, g1;
+  fma2(g0, g1, c5, c5, a0, a1, c4, c4);
+  fma2(g0, g1, g0, g1, a0, a1, c3, c3);
+  fma2(g0, g1, g0, g1, a0, a1, c2, c2);
+  fma2(g0, g1, g0, g1, a0, a1, c1, c1);
+  fma2(g0, g1, g0, g1, a0, a1, c0, c0);
+  x0 = fmaf(-a0, ex2(g0), fmaxf(x0, 0.f));
+  x1 = fmaf(-a1, ex2(g1), fmaxf(x1, 0.f));
 }
 
-// Epilogue of 32 rows x `cols` columns (from tile column c_first of the unit) by one warp.
-// `release` is called once, as soon as the columns shared with the other accumulator
-// have been read. Chunks run upwards or, with `down`, downwards, so that those come first.
-template <int kEpi, typename Release>
+template <bool kGelu, bool kE4m3, int n>
+__device__ __forceinline__ void bias_act(float (&t)[n], const float* bias) {
+#pragma unroll
+  for (int k = 0; k < n; k += 4) {
+    const float4 b = lds4(bias + k);
+    add2(t[k], t[k + 1], t[k], t[k + 1], b.x, b.y);
+    add2(t[k + 2], t[k + 3], t[k + 2], t[k + 3], b.z, b.w);
+    if constexpr (kGelu && kE4m3) {
+      gelu_e4m3_2(t[k], t[k + 1]);
+      gelu_e4m3_2(t[k + 2], t[k + 3]);
+    } else if constexpr (kGelu) {
+      gelu_fast2(t[k], t[k + 1]);
+      gelu_fast2(t[k + 2], t[k + 3]);
+    }
+  }
+}
+
+// Epilogue of 32 rows x `cols` columns (from output column n0) by one warp. `bias`: the
+// warp's copy of those columns' bias in shared memory, zeros where there is none. `release`
+// is called once, as soon as the columns shared with the other accumulator have been read.
+// Chunks run upwards or, with `down`, downwards, so that those come first.
+template <int kEpi, bool kGelu, typename Release>
 __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0, int cols,
-                                         uint32_t taddr, bool down, uint8_t* stage, int lane, Release&& release) {
+                                         uint32_t taddr, bool down, uint8_t* stage, const float* bias, int lane,
+                                         Release&& release) {
   if constexpr (kEpi == ENC_FP8_OUT_FP8) {
-    // one block of 128 columns of a row per thread, held in registers: its scale needs all of them
+    // One block of 128 columns of a row per thread, held in registers: its scale needs all of
+    // them. (Half a block in each of 16 warps, the halves' amax joined in shared memory, keeps
+    // up with the MMAs where this is the slower side, but 24000 x 5120 x 1280 with GELU takes
+    // 156 us so against 147: the chip is at its power limit, and that form does more work.)
     float v[128];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      tmem_ld_32x32b_x32(taddr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+    for (int c = 0; c < 128; c += 32) tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
     if (lane == 0) bulk_wait_read0();
     tmem_wait_ld();
     release();
     __syncwarp();   // the previous store has read the staging tile
-    float top = 0.f;
+    bias_act<kGelu, true>(v, bias);
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 128; j += 4) {
-      const float4 b = bias4(p, n0 + j);
-      add2(v[j], v[j + 1], v[j], v[j + 1], b.x, b.y);
-      add2(v[j + 2], v[j + 3], v[j + 2], v[j + 3], b.z, b.w);
-      if (p.gelu) {
-        gelu_fast2(v[j], v[j + 1]);
-        gelu_fast2(v[j + 2], v[j + 3]);
-      }
-      top = fmaxf(fmaxf(top, fmaxf(fabsf(v[j]), fabsf(v[j + 1]))), fmaxf(fabsf(v[j + 2]), fabsf(v[j + 3])));
+    for (int j = 0; j < 128; j += 8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], fabsf(v[j + 2 * k])), fabsf(v[j + 2 * k + 1]));
     }
-    uint32_t bits = __float_as_uint(top);   // fmaxf passes over NaN
+    uint32_t bits = __float_as_uint(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));   // passes over NaN
     if (bits >= 0x7F800000u) {              // an infinity in the row: the largest finite magnitude instead
       bits = 0;
 #pragma unroll
@@ -175,7 +210,7 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
     for (int i = 0; i < nc; ++i) {
       const int c = (down ? nc - 1 - i : i) * kChunk;
       if (n0 + c >= p.N) continue;
-      uint32_t v[kChunk];
+      float v[kChunk];
 #pragma unroll
       for (int j = 0; j < kChunk; j += 32)
         tmem_ld_32x32b_x32(taddr + c + j, *reinterpret_cast<uint32_t(*)[32]>(&v[j]));
@@ -183,33 +218,25 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
       tmem_wait_ld();
       if (i == 0) release();
       __syncwarp();
+      if constexpr (kEpi == ENC_FP8_OUT_BF16) {
+        bias_act<kGelu, false>(v, bias + c);
+      } else {
+        bias_act<false, false>(v, bias + c);
+        if constexpr (kGelu) {   // fp32 keeps what the fast form would lose
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k) v[k] = gelu_erf(v[k]);
+        }
+      }
       uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        constexpr int kPer = kChunk / 8;   // columns per 16-byte piece
-        float t[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; k += 4) {
-          const float4 b = bias4(p, n0 + c + kPer * j + k);
-          const uint32_t* a = v + kPer * j + k;
-          add2(t[k], t[k + 1], __uint_as_float(a[0]), __uint_as_float(a[1]), b.x, b.y);
-          add2(t[k + 2], t[k + 3], __uint_as_float(a[2]), __uint_as_float(a[3]), b.z, b.w);
-        }
-        if constexpr (kEpi == ENC_FP8_OUT_BF16) {
-          if (p.gelu) {
-#pragma unroll
-            for (int k = 0; k < kPer; k += 2) gelu_fast2(t[k], t[k + 1]);
-          }
+        const float* t = v + kChunk / 8 * j;
+        if constexpr (kEpi == ENC_FP8_OUT_BF16)
           row[j ^ (lane & 7)] = make_uint4(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]), pack_bf16x2(t[4], t[5]),
                                            pack_bf16x2(t[6], t[7]));
-        } else {
-          if (kEpi == ENC_FP8_OUT_FP32 && p.gelu) {   // fp32 keeps what the fast form would lose
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) t[k] = gelu_erf(t[k]);
-          }
+        else
           row[j ^ (lane & 7)] = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
                                            __float_as_uint(t[3]));
-        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -222,7 +249,7 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
   }
 }
 
-template <int kEpi>
+template <int kEpi, bool kGelu>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ CUtensorMap map_c, const GemmFp8Params p) {
@@ -230,12 +257,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sW = sA + kStages * kOperandBytes;
-  uint8_t* stage_c = sW + kStages * kOperandBytes;                    // 4 KB per epilogue warp
-  uint8_t* sS = stage_c + kEpiWarps * 4096;                           // scale slots
-  uint64_t* full = reinterpret_cast<uint64_t*>(sS + kScaleSlots * kScaleSlotBytes);   // used in the first CTA
+  uint8_t* stage_c = sW + kStages * kOperandBytes;                            // 4 KB per epilogue warp
+  uint8_t* sS = stage_c + kEpiWarps * 4096;                                   // scale slots
+  float* sB = reinterpret_cast<float*>(sS + kScaleSlots * kScaleSlotBytes);   // bias, 128 columns per epilogue warp
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kEpiWarps * 128);         // used in the first CTA
   uint64_t* empty = full + kStages;
-  uint64_t* sfull = empty + kStages;        // [2] scales of both CTAs written; used in the first CTA
-  uint64_t* sempty = sfull + kScaleSlots;   // [2] MMAs that read the slot are done
+  uint64_t* sfull = empty + kStages;        // [4] this CTA's scales are written
+  uint64_t* speer = sfull + kScaleSlots;    // [4] and the second CTA's; used in the first CTA
+  uint64_t* sempty = speer + kScaleSlots;   // [4] MMAs that read the slot are done
   uint64_t* tfull = sempty + kScaleSlots;   // [2] accumulator complete
   uint64_t* tempty = tfull + 2;             // shared columns read; used in the first CTA
   uint64_t* drain = tempty + 1;
@@ -250,7 +279,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int s = 0; s < kScaleSlots; ++s) { mbar_init(&sfull[s], 2); mbar_init(&sempty[s], 1); }
+    for (int s = 0; s < kScaleSlots; ++s) { mbar_init(&sfull[s], 1); mbar_init(&speer[s], 1); mbar_init(&sempty[s], 1); }
     for (int a = 0; a < 2; ++a) mbar_init(&tfull[a], 1);
     mbar_init(tempty, 2 * kEpiWarps);
     mbar_init(drain, 1);
@@ -306,8 +335,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     if (leader) {
       const uint64_t adesc0 = smem_desc_sw128(smem_u32(sA)), wdesc0 = smem_desc_sw128(smem_u32(sW));
       int stage = 0, slot = 0, acc = 0;
-      uint32_t phase = 0, sphase = 0, tphase = 0;
+      uint32_t phase = 0, sphase = 0, tphase = 0;   // sphase: of slot 0's round
       bool ok = true, issued = false;
+      bool wrapped = false;   // groups before the third have no earlier user of their TMEM columns
       for (int u = cluster; ok && u < units; u += nclusters) {
         const uint32_t idesc = unit_at(p, u).width == 256 ? idesc_mxf8(256, 256) : idesc_mxf8(256, 128);
         // the tile before: its columns shared with this one's accumulator have been read
@@ -317,8 +347,20 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         const uint32_t d_tmem = tmem_base + (acc ? kAcc1 : 0u);
         for (int kb = 0; kb < p.num_kb; ++kb) {
           const uint32_t id = kb & 3;
-          const uint32_t sfa = tmem_base + kScaleCol + slot * kScaleSlotCols, sfb = sfa + 4;
-          if (id == 0 && !mbar_wait_warp(&sfull[slot], sphase, abort_v, kWaitLimitNs)) { ok = false; break; }
+          const uint32_t sfa = tmem_base + kScaleCol + (slot & (kScaleTmemSlots - 1)) * kScaleSlotCols, sfb = sfa + 4;
+          if (id == 0) {
+            // the scales are in shared memory, and the group two before, which used the same
+            // TMEM columns, is done (its slot's round is the last one where slot < 2)
+            const int before = (slot + kScaleSlots - kScaleTmemSlots) & (kScaleSlots - 1);
+            if (!mbar_wait_warp(&sfull[slot], sphase, abort_v, kWaitLimitNs) ||
+                !mbar_wait_warp(&speer[slot], sphase, abort_v, kWaitLimitNs) ||
+                ((wrapped || slot >= kScaleTmemSlots) &&
+                 !mbar_wait_warp(&sempty[before], sphase ^ (slot < kScaleTmemSlots ? 1u : 0u), abort_v,
+                                 kWaitLimitNs))) {
+              ok = false;
+              break;
+            }
+          }
           if (!mbar_wait_warp(&full[stage], phase, abort_v, kWaitLimitNs)) { ok = false; break; }
           tc_fence_after();
           const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
@@ -340,7 +382,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
           __syncwarp();
           issued = true;
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
-          if (last && ++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+          if (last && ++slot == kScaleSlots) { slot = 0; sphase ^= 1u; wrapped = true; }
         }
         if (!ok) break;
         if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
@@ -353,48 +395,81 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         __syncwarp();
         mbar_wait_warp(drain, 0, nullptr, kWaitLimitNs);
       }
+    } else {
+      // An arrival at the other CTA's barrier that releases earlier writes takes about 1,400
+      // cycles; here it holds up nobody.
+      const uint32_t speer_leader = peer_addr(speer, 0);
+      int slot = 0;
+      uint32_t sphase = 0;
+      bool ok = true;
+      const int groups = (p.num_kb + 3) / 4;
+      for (int u = cluster; ok && u < units; u += nclusters) {
+        for (int g = 0; g < groups; ++g) {
+          if (!mbar_wait_warp(&sfull[slot], sphase, abort_v, kWaitLimitNs)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_cluster(speer_leader + 8 * slot);
+          __syncwarp();
+          if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+        }
+      }
+      if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------- scales
     // Both CTAs: this CTA's 128 rows of A, all the unit's rows of W. The words of the next
-    // four blocks are loaded before the slot for them is free.
-    const uint32_t sfull_leader[kScaleSlots] = {peer_addr(&sfull[0], 0), peer_addr(&sfull[1], 0)};
+    // four blocks are on their way while these are handed over.
     int slot = 0;
     uint32_t sphase = 0;
     bool ok = true;
     const int groups = (p.num_kb + 3) / 4;
-    for (int u = cluster; ok && u < units; u += nclusters) {
+    auto load = [&](int u, int g, uint32_t (&w)[12]) {
       const Unit t = unit_at(p, u);
-      const int m0 = t.m0 + 128 * static_cast<int>(rank);
-      for (int g = 0; g < groups; ++g) {
-        uint32_t w[12];
+      const int m0 = t.m0 + 128 * static_cast<int>(rank) + lane;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = scale_word(p.a_scales, p.k_pitch, m0 + 32 * c + lane, p.M, g);
+      for (int c = 0; c < 4; ++c) w[c] = scale_word(p.a_scales, p.k_pitch, m0 + 32 * c, p.M, g);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          w[4 + c] = c * 32 < t.width ? scale_word(p.w_scales, p.k_pitch, t.n0 + 32 * c + lane, p.N, g) : kUnitScale;
-        if (!mbar_wait_warp(&sempty[slot], sphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
-        uint4* dst = reinterpret_cast<uint4*>(sS + slot * kScaleSlotBytes) + lane;
+      for (int c = 0; c < 8; ++c)
+        w[4 + c] = c * 32 < t.width ? scale_word(p.w_scales, p.k_pitch, t.n0 + 32 * c + lane, p.N, g) : kUnitScale;
+    };
+    uint32_t w[12];
+    int u = cluster, g = 0;
+    if (u < units) load(u, g, w);
+    while (u < units) {
+      int nu = u, ng = g + 1;
+      if (ng == groups) { ng = 0; nu += nclusters; }
+      uint32_t next[12];
+      if (nu < units) load(nu, ng, next);
+      if (!mbar_wait_warp(&sempty[slot], sphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+      uint4* dst = reinterpret_cast<uint4*>(sS + slot * kScaleSlotBytes) + lane;
 #pragma unroll
-        for (int c = 0; c < 3; ++c) dst[c * 32] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        fence_proxy_async_smem();   // tcgen05.cp reads them through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(sfull_leader[slot]);
-        if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
-      }
+      for (int c = 0; c < 3; ++c) dst[c * 32] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+      fence_proxy_async_smem();   // tcgen05.cp reads them through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull[slot]);
+      if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+#pragma unroll
+      for (int c = 0; c < 12; ++c) w[c] = next[c];
+      u = nu;
+      g = ng;
     }
     if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
-  } else {
+  } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;                 // TMEM lanes this warp may read
     const int half = (warp - kEpiWarp0) >> 2;     // which half of the unit's columns
     uint8_t* stage = stage_c + (warp - kEpiWarp0) * 4096;
+    float* bias = sB + (warp - kEpiWarp0) * 128;
     const uint32_t tempty_leader = peer_addr(tempty, 0);
     int acc = 0;
     uint32_t tphase = 0;
     for (int u = cluster; u < units; u += nclusters) {
       const Unit t = unit_at(p, u);
       const int r0 = t.m0 + 128 * static_cast<int>(rank) + quarter * 32;
+      // e4m3 output: a row's block of 128 columns is one thread's, so a narrow unit is the first half's alone
+      const int per = kEpi == ENC_FP8_OUT_FP8 ? 128 : t.width / 2;
+      const int c0 = half * per, n0 = t.n0 + c0;
+      float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);   // N is a multiple of 16
+      if (p.bias && n0 + 4 * lane < p.N) b4 = __ldg(reinterpret_cast<const float4*>(p.bias + n0) + lane);
+      reinterpret_cast<float4*>(bias)[lane] = b4;    // the previous unit's reads ended with a __syncwarp
       if (!mbar_wait(&tfull[acc], tphase, abort_v, kWaitLimitNs)) {
         set_status(p.status, kDevTimeout);
         *abort_v = 1;
@@ -408,18 +483,15 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         released = true;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty_leader);
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader);
       };
-      // e4m3 output: a row's block of 128 columns is one thread's, so a narrow unit is the first half's alone
-      const int per = kEpi == ENC_FP8_OUT_FP8 ? 128 : t.width / 2;
-      const int c0 = half * per, n0 = t.n0 + c0;
-      // the first accumulator's last columns are the second one's first
-      const bool shares = acc ? half == 0 : (half == 1 && t.width == 256);
+      // the first accumulator's last 32 columns are the second one's first
+      const bool shares = acc ? c0 == 0 : c0 + per == 256;
       if (!shares) release();
       if (c0 < t.width && n0 < p.N && r0 < p.M) {
         const uint32_t taddr =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(c0);
-        epilogue<kEpi>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, lane, release);
+        epilogue<kEpi, kGelu>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, bias, lane, release);
       }
       release();
       acc ^= 1;
@@ -444,7 +516,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   }
 }
 
-template <int kEpi>
+template <int kEpi, bool kGelu>
 cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cudaStream_t stream) {
   static DeviceOnce once;
   static int max_clusters[64] = {};   // written under once's mutex, read after its acquire
@@ -452,7 +524,7 @@ cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cud
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidValue;
   cudaError_t setup_error = cudaSuccess;
   const bool ready = once.run(dev, [&] {
-    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_kernel<kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_kernel<kEpi, kGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e != cudaSuccess) {
       setup_error = e;
@@ -470,7 +542,7 @@ cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cud
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_kernel<kEpi>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_kernel<kEpi, kGelu>, &cfg);
     if (e != cudaSuccess || n < 1) n = sm_count / 2;   // every SM pairs up
     cudaGetLastError();
     if (n < 1) {
@@ -491,7 +563,7 @@ cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cud
   p.tail = (!narrow && 2 * tail <= ncl) ? tail : 0;
   const int units = p.num_tiles + p.tail;
   const int clusters = units < ncl ? units : ncl;
-  gemm_fp8_kernel<kEpi><<<2 * clusters, kThreads, kSmemBytes, stream>>>(m.a, m.w, m.c, p);
+  gemm_fp8_kernel<kEpi, kGelu><<<2 * clusters, kThreads, kSmemBytes, stream>>>(m.a, m.w, m.c, p);
   return cudaGetLastError();
 }
 
@@ -501,10 +573,16 @@ cudaError_t launch_gemm_fp8(const GemmFp8Maps& m, const GemmFp8Params& p, int ou
                             cudaStream_t stream) {
   if (p.M <= 0) return cudaSuccess;
   switch (out_kind) {
-    case ENC_FP8_OUT_BF16: return launch_pair<ENC_FP8_OUT_BF16>(m, p, sm_count, stream);
-    case ENC_FP8_OUT_FP32: return launch_pair<ENC_FP8_OUT_FP32>(m, p, sm_count, stream);
-    case ENC_FP8_OUT_FP8: return launch_pair<ENC_FP8_OUT_FP8>(m, p, sm_count, stream);
-    case ENC_FP8_OUT_RESID: return launch_pair<ENC_FP8_OUT_RESID>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_BF16:
+      return p.gelu ? launch_pair<ENC_FP8_OUT_BF16, true>(m, p, sm_count, stream)
+                    : launch_pair<ENC_FP8_OUT_BF16, false>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_FP32:
+      return p.gelu ? launch_pair<ENC_FP8_OUT_FP32, true>(m, p, sm_count, stream)
+                    : launch_pair<ENC_FP8_OUT_FP32, false>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_FP8:
+      return p.gelu ? launch_pair<ENC_FP8_OUT_FP8, true>(m, p, sm_count, stream)
+                    : launch_pair<ENC_FP8_OUT_FP8, false>(m, p, sm_count, stream);
+    case ENC_FP8_OUT_RESID: return launch_pair<ENC_FP8_OUT_RESID, false>(m, p, sm_count, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -113,7 +113,7 @@ struct GemmFp8Params {
   int out_pitch;
   int* status;
 };
-// Operands (128 x 128 byte boxes) and output (32 rows x 128 bytes), 128-byte swizzle.
+// Operands (128 x 128 byte boxes) and output (32 rows of 128 bytes), 128-byte swizzle.
 struct GemmFp8Maps {
   CUtensorMap a, w, c;
 };
