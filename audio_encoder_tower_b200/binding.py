@@ -382,56 +382,83 @@ def _expect(ok, what: str):
         raise ValueError(what)
 
 
-def _fp8_call(device, stream, fresh, call):
-    """call(stream handle) with `device` current. stream=None is the device's current stream;
-    tensors allocated here (`fresh`) are marked as used on a stream given by the caller."""
+# What the 8-bit functions use of torch, looked up once: they cost a few microseconds of host
+# time per call, about as much as a small launch, so their common case takes the short way.
+_torch = _BF16 = _FP32 = _E4M3 = _E8M0 = _U8 = _raw_stream = _cur_device = None
+
+
+def _bind_torch():
+    global _torch, _BF16, _FP32, _E4M3, _E8M0, _U8, _raw_stream, _cur_device
     import torch
-    _expect(device.type == "cuda", "the tensors must be on a CUDA device")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _fp8_call(device, stream, fresh, call)
+    _BF16, _FP32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+    _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    _raw_stream, _cur_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
+    load_library()
+
+
+def _fp8_call(fn, what, device, stream, fresh, *args):
+    """fn(*args, stream handle) on `device` (an ordinal, made current). stream=None is the
+    device's current stream; tensors allocated here (`fresh`) are marked as used on a stream
+    given by the caller."""
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if device != _cur_device():
+        with _torch.cuda.device(device):
+            return _fp8_call(fn, what, device, stream, fresh, *args)
     if stream is None:
-        return call(torch.cuda.current_stream().cuda_stream)
-    if fresh:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream))
-        for t in fresh:
-            t.record_stream(s)
-    return call(_stream_handle(stream))
+        handle = _raw_stream(device)
+    else:
+        handle = _stream_handle(stream)
+        if fresh:
+            s = stream if isinstance(stream, _torch.cuda.Stream) else _torch.cuda.ExternalStream(handle)
+            for t in fresh:
+                t.record_stream(s)
+    code = fn(*args, handle)
+    if code != ENC_OK:
+        raise EncError(code, what)
 
 
 def _row_stride(t, device, what: str):
     """(enc_dtype, row stride) of a bf16 or fp32 matrix whose rows are contiguous."""
-    import torch
-    _expect(t.dtype in (torch.bfloat16, torch.float32) and t.dim() == 2 and t.device == device
-            and (t.stride(1) == 1 or t.shape[1] <= 1),
-            f"{what} must be a bf16 or fp32 matrix with contiguous rows on {device}")
-    return (ENC_DTYPE_BF16 if t.dtype == torch.bfloat16 else ENC_DTYPE_FP32,
-            t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    dt = t.dtype
+    if (dt == _BF16 or dt == _FP32) and t.dim() == 2 and t.get_device() == device:
+        code = ENC_DTYPE_BF16 if dt == _BF16 else ENC_DTYPE_FP32
+        if t.is_contiguous():
+            return code, t.size(1)
+        if t.stride(1) == 1 or t.size(1) <= 1:
+            return code, (t.stride(0) if t.size(0) > 1 else t.size(1))
+    raise ValueError(f"{what} must be a bf16 or fp32 matrix with contiguous rows on device {device}")
 
 
-def _fp8_matrix(q, scales, rows, cols, device, what: str):
-    """Check an e4m3 matrix with block scales (None: allocate it); returns (q, scales, the new ones)."""
-    import torch
+def _check_fp8(q, scales, rows, cols, device, what: str):
+    """An e4m3 [rows, cols] matrix with its block scales, both contiguous and on `device`."""
+    if q.dtype != _E4M3 or q.shape != (rows, cols) or not q.is_contiguous() or q.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous float8_e4m3fn [{rows}, {cols}] tensor on device {device}")
+    if (scales.dtype != _E8M0 and scales.dtype != _U8) or not scales.is_contiguous() or \
+            scales.shape != (rows, (cols + 511) // 512 * 4) or scales.get_device() != device:
+        raise ValueError(f"the scales of {what} must be a contiguous float8_e8m0fnu "
+                         f"[{rows}, {fp8_scale_pitch(cols)}] tensor on device {device}")
+
+
+def _fp8_out(q, scales, rows, cols, like, what: str):
+    """(q, scales, the tensors allocated here): the caller's output matrix, or a new one beside `like`."""
     fresh = []
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
+        q = _torch.empty((rows, cols), dtype=_E4M3, device=like.device)
         fresh.append(q)
     if scales is None:
-        scales = torch.empty((rows, fp8_scale_pitch(cols)), dtype=torch.float8_e8m0fnu, device=device)
+        scales = _torch.empty((rows, fp8_scale_pitch(cols)), dtype=_E8M0, device=like.device)
         fresh.append(scales)
-    _expect(q.dtype == torch.float8_e4m3fn and q.shape == (rows, cols) and q.is_contiguous() and q.device == device,
-            f"{what} must be a contiguous float8_e4m3fn [{rows}, {cols}] tensor on {device}")
-    _expect(scales.dtype in (torch.float8_e8m0fnu, torch.uint8) and scales.shape == (rows, fp8_scale_pitch(cols))
-            and scales.is_contiguous() and scales.device == device,
-            f"the scales of {what} must be a contiguous float8_e8m0fnu [{rows}, {fp8_scale_pitch(cols)}] tensor on "
-            f"{device}")
+    _check_fp8(q, scales, rows, cols, like.get_device(), what)
     return q, scales, fresh
 
 
-def _fp32_vector(v, n, device, what: str):
-    import torch
-    _expect(v is None or (v.dtype == torch.float32 and v.shape == (n,) and v.is_contiguous() and v.device == device),
-            f"{what} must be a contiguous fp32 [{n}] tensor on {device}")
+def _check_vector(v, n, device, what: str):
+    """A contiguous fp32 [n] vector on `device`, or None."""
+    if v is not None and (v.dtype != _FP32 or v.shape != (n,) or not v.is_contiguous()
+                          or v.get_device() != device):
+        raise ValueError(f"{what} must be a contiguous fp32 [{n}] tensor on device {device}")
 
 
 def quantize_fp8(x, q=None, scales=None, stream=None):
@@ -441,12 +468,14 @@ def quantize_fp8(x, q=None, scales=None, stream=None):
     Returns (q float8_e4m3fn [rows, cols], scales float8_e8m0fnu [rows, fp8_scale_pitch(cols)]):
     element (r, c) stands for q[r, c] * scales[r, c // 128].
     """
-    dtype, ldx = _row_stride(x, x.device, "x")
+    if _torch is None:
+        _bind_torch()
+    dev = x.get_device()
+    dtype, ldx = _row_stride(x, dev, "x")
     rows, cols = x.shape
-    q, scales, fresh = _fp8_matrix(q, scales, rows, cols, x.device, "q")
-    lib = load_library()
-    _check(_fp8_call(x.device, stream, fresh, lambda s: lib.enc_quantize_fp8(
-        x.data_ptr(), dtype, ldx, rows, cols, q.data_ptr(), scales.data_ptr(), s)), "enc_quantize_fp8")
+    q, scales, fresh = _fp8_out(q, scales, rows, cols, x, "q")
+    _fp8_call(_LIB.enc_quantize_fp8, "enc_quantize_fp8", dev, stream, fresh, x.data_ptr(), dtype, ldx, rows,
+              cols, q.data_ptr(), scales.data_ptr())
     return q, scales
 
 
@@ -458,31 +487,33 @@ def norm_fp8(x, gamma, beta=None, delta=None, kind="rms", eps=1e-5, x_out=None, 
     Returns (q, scales, x_out): x_out is the stream after the addition, in x's type; without a
     delta it is x itself, and x_out=x updates the stream in place. gamma, beta: fp32 [d].
     """
-    import torch
-    _expect(kind in ("rms", "layer"), 'kind must be "rms" or "layer"')
-    dev = x.device
+    if _torch is None:
+        _bind_torch()
+    if gamma is None or (kind != "rms" and kind != "layer"):
+        raise ValueError('gamma is required, and kind must be "rms" or "layer"')
+    dev = x.get_device()
     dtype, ldx = _row_stride(x, dev, "x")
     rows, d = x.shape
-    _expect(gamma is not None, "gamma is required")
-    _fp32_vector(gamma, d, dev, "gamma")
-    _fp32_vector(beta, d, dev, "beta")
-    q, scales, fresh = _fp8_matrix(q, scales, rows, d, dev, "q")
-    ddtype, ldd = ENC_DTYPE_BF16, d
+    _check_vector(gamma, d, dev, "gamma")
+    _check_vector(beta, d, dev, "beta")
+    q, scales, fresh = _fp8_out(q, scales, rows, d, x, "q")
+    ddtype, ldd, ldxo = ENC_DTYPE_BF16, d, d
     if delta is not None:
         ddtype, ldd = _row_stride(delta, dev, "delta")
-        _expect(delta.shape == x.shape, "delta must have x's shape")
+        if delta.shape != x.shape:
+            raise ValueError("delta must have x's shape")
         if x_out is None:
-            x_out = torch.empty((rows, d), dtype=x.dtype, device=dev)
+            x_out = _torch.empty((rows, d), dtype=x.dtype, device=x.device)
             fresh.append(x_out)
-    ldxo = d
     if x_out is not None:
         odtype, ldxo = _row_stride(x_out, dev, "x_out")
-        _expect(odtype == dtype and x_out.shape == x.shape, "x_out must have x's shape and type")
-    lib = load_library()
-    _check(_fp8_call(dev, stream, fresh, lambda s: lib.enc_norm_fp8(
-        ENC_NORM_RMS if kind == "rms" else ENC_NORM_LAYER, x.data_ptr(), dtype, ldx, _ptr(delta), ddtype, ldd,
-        gamma.data_ptr(), _ptr(beta), eps, rows, d, _ptr(x_out), ldxo, q.data_ptr(), scales.data_ptr(), s)),
-        "enc_norm_fp8")
+        if odtype != dtype or x_out.shape != x.shape:
+            raise ValueError("x_out must have x's shape and type")
+    _fp8_call(_LIB.enc_norm_fp8, "enc_norm_fp8", dev, stream, fresh,
+              ENC_NORM_RMS if kind == "rms" else ENC_NORM_LAYER, x.data_ptr(), dtype, ldx,
+              None if delta is None else delta.data_ptr(), ddtype, ldd, gamma.data_ptr(),
+              None if beta is None else beta.data_ptr(), eps, rows, d, None if x_out is None else x_out.data_ptr(),
+              ldxo, q.data_ptr(), scales.data_ptr())
     return q, scales, x if x_out is None else x_out
 
 
@@ -495,41 +526,40 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
     returns out, or (out, out_scales) for e4m3. With resid (fp32 [M, N]) the product and the
     bias are added to it instead, and resid is returned. bias: fp32 [N].
     """
-    import torch
-    dev = a.device
+    if _torch is None:
+        _bind_torch()
+    dev = a.get_device()
     M, K = a.shape
-    N = w.shape[0]
-    _fp8_matrix(a, a_scales, M, K, dev, "a")
-    _fp8_matrix(w, w_scales, N, K, dev, "w")
-    _fp32_vector(bias, N, dev, "bias")
-    fresh = []
+    N = w.size(0)
+    _check_fp8(a, a_scales, M, K, dev, "a")
+    _check_fp8(w, w_scales, N, K, dev, "w")
+    _check_vector(bias, N, dev, "bias")
+    fresh = ()
     if resid is not None:
         _expect(out is None and out_dtype is None and out_scales is None and not gelu,
                 "resid takes no out, out_dtype, out_scales or gelu")
-        _expect(resid.dtype == torch.float32 and resid.shape == (M, N) and resid.is_contiguous()
-                and resid.device == dev, f"resid must be a contiguous fp32 [{M}, {N}] tensor on {dev}")
-        kind, dst = ENC_FP8_OUT_RESID, resid
+        kind, tdt, dst = ENC_FP8_OUT_RESID, _FP32, resid
     else:
-        types = {"bf16": (ENC_FP8_OUT_BF16, torch.bfloat16), "fp32": (ENC_FP8_OUT_FP32, torch.float32),
-                 "fp8": (ENC_FP8_OUT_FP8, torch.float8_e4m3fn)}
         if out_dtype is None:
-            out_dtype = "bf16" if out is None else {t: n for n, (_, t) in types.items()}.get(out.dtype)
-        _expect(out_dtype in types, 'the output type must be "bf16", "fp32" or "fp8"')
-        kind, tdt = types[out_dtype]
-        if kind == ENC_FP8_OUT_FP8:
-            out, out_scales, fresh = _fp8_matrix(out, out_scales, M, N, dev, "out")
+            out_dtype = "bf16" if out is None or out.dtype == _BF16 else \
+                "fp32" if out.dtype == _FP32 else "fp8"
+        _expect(out_dtype in ("bf16", "fp32", "fp8"), 'the output type must be "bf16", "fp32" or "fp8"')
+        if out_dtype == "fp8":
+            out, out_scales, fresh = _fp8_out(out, out_scales, M, N, a, "out")
+            kind, tdt, dst = ENC_FP8_OUT_FP8, _E4M3, out
         else:
             _expect(out_scales is None, "out_scales belong to an e4m3 output")
+            kind, tdt = (ENC_FP8_OUT_BF16, _BF16) if out_dtype == "bf16" else \
+                (ENC_FP8_OUT_FP32, _FP32)
             if out is None:
-                out = torch.empty((M, N), dtype=tdt, device=dev)
-                fresh.append(out)
-            _expect(out.dtype == tdt and out.shape == (M, N) and out.is_contiguous() and out.device == dev,
-                    f"out must be a contiguous {out_dtype} [{M}, {N}] tensor on {dev}")
-        dst = out
-    lib = load_library()
-    _check(_fp8_call(dev, stream, fresh, lambda s: lib.enc_linear_fp8(
-        a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), _ptr(bias), dst.data_ptr(),
-        _ptr(out_scales), kind, M, N, K, 1 if gelu else 0, _ptr(status), s)), "enc_linear_fp8")
+                out = _torch.empty((M, N), dtype=tdt, device=a.device)
+                fresh = (out,)
+            dst = out
+    if dst.dtype != tdt or dst.shape != (M, N) or not dst.is_contiguous() or dst.get_device() != dev:
+        raise ValueError(f"the output must be a contiguous {tdt} [{M}, {N}] tensor on device {dev}")
+    _fp8_call(_LIB.enc_linear_fp8, "enc_linear_fp8", dev, stream, fresh, a.data_ptr(), a_scales.data_ptr(),
+              w.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(), dst.data_ptr(),
+              None if out_scales is None else out_scales.data_ptr(), kind, M, N, K, 1 if gelu else 0, _ptr(status))
     return (out, out_scales) if kind == ENC_FP8_OUT_FP8 else dst
 
 

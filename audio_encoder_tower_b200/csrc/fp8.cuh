@@ -37,4 +37,47 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// ------------------------------------------------- block-scaled tensor-core products
+constexpr int kBK = 128;                    // K elements (and bytes) per ring stage: one scale block
+constexpr uint32_t kUnitScale = 0x7F7F7F7Fu;   // scales of rows outside the matrix: 2^0
+
+// Instruction descriptor, kind::mxf8f6f4: fp32 accumulator, e4m3 A and B, both
+// K-major, e8m0 scales; `id` is the byte (0..3) of the scale words to use.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
+  return (static_cast<uint32_t>(n >> 3) << 17)     // N / 8
+         | (1u << 23)                              // scale type: e8m0
+         | (static_cast<uint32_t>(m >> 7) << 27);  // M / 128
+}
+__device__ __forceinline__ uint32_t idesc_scale_id(uint32_t id) { return (id << 4) | (id << 29); }   // B, A
+
+// Shared-memory descriptor of 32 rows of 16 bytes of scales (512 contiguous bytes): no swizzle, 8-row core matrices of
+// 16-byte rows, 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Word of scales (blocks 4 g .. 4 g + 3) of a row; rows outside the matrix scale by 1.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int pitch, int row, int rows, int g) {
+  return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(s + (int64_t)row * pitch) + g) : kUnitScale;
+}
+
+// GELU for an e4m3 result, on packed pairs: max(x, 0) - |x| 2^G(|x|) as gelu_fast2, with
+// G = log2 Phi(-a) from a minimax polynomial of degree 5 over [0, 5.5] (relative error of the
+// result there at most 2.5e-4, a 250th of half an e4m3 step). Beyond, the polynomial keeps
+// falling, so no clamp is needed: the result is within 1.9e-8 |x| of max(x, 0), as GELU is.
+__device__ __forceinline__ void gelu_e4m3_2(float& x0, float& x1) {
+  constexpr float c0 = -1.000359058380127f, c1 = -1.1462607383728027f, c2 = -0.4696812331676483f,
+                  c3 = -0.04459895193576813f, c4 = 0.004869762342423201f, c5 = -0.00023325053916778415f;
+  const float a0 = fabsf(x0), a1 = fabsf(x1);
+  float g0, g1;
+  fma2(g0, g1, c5, c5, a0, a1, c4, c4);
+  fma2(g0, g1, g0, g1, a0, a1, c3, c3);
+  fma2(g0, g1, g0, g1, a0, a1, c2, c2);
+  fma2(g0, g1, g0, g1, a0, a1, c1, c1);
+  fma2(g0, g1, g0, g1, a0, a1, c0, c0);
+  x0 = fmaf(-a0, ex2(g0), fmaxf(x0, 0.f));
+  x1 = fmaf(-a1, ex2(g1), fmaxf(x1, 0.f));
+}
+
 }  // namespace enc

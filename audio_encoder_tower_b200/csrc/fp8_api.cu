@@ -96,9 +96,10 @@ enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, co
     return ENC_ERR_INVALID_ARG;
   const int sms = sm_count_current();
   if (sms <= 0) return device_status(sms);
+  const GemmFp8SmallPlan small = plan_gemm_fp8_small(M, N, K, sms);
   GemmFp8Maps m;
-  if (!make_fp8_operand_map(&m.a, A, M, K) || !make_fp8_operand_map(&m.w, W, N, K) ||
-      !make_fp8_out_map(&m.c, out, out_kind, M, N))
+  if (!make_fp8_operand_map(&m.a, A, M, K, small.tile_m ? small.tile_m : 128) ||
+      !make_fp8_operand_map(&m.w, W, N, K, small.tile_m ? 128 : 64) || (!small.tile_m && !make_fp8_out_map(&m.c, out, out_kind, M, N)))
     return ENC_ERR_CUDA;
   GemmFp8Params p;
   memset(&p, 0, sizeof(p));
@@ -111,6 +112,7 @@ enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, co
   p.out_scales = reinterpret_cast<uint8_t*>(out_scales);
   p.out_pitch = fp8_pitch(N);
   p.status = status;
+  if (small.tile_m) return launched(launch_gemm_fp8_small(m.a, m.w, small, p, out, out_kind, stream));
   return launched(launch_gemm_fp8(m, p, out_kind, sms, stream));
 }
 

@@ -24,17 +24,6 @@ namespace enc {
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far above any legitimate wait
-constexpr int kBK = 128;                           // K elements (and bytes) per stage: one scale block
-constexpr uint32_t kUnitScale = 0x7F7F7F7Fu;       // scales of rows outside the matrix: 2^0
-
-// Instruction descriptor, kind::mxf8f6f4: fp32 accumulator, e4m3 A and B, both
-// K-major, e8m0 scales; `id` is the byte (0..3) of the scale words to use.
-__host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
-  return (static_cast<uint32_t>(n >> 3) << 17)     // N / 8
-         | (1u << 23)                              // scale type: e8m0
-         | (static_cast<uint32_t>(m >> 7) << 27);  // M / 128
-}
-__device__ __forceinline__ uint32_t idesc_scale_id(uint32_t id) { return (id << 4) | (id << 29); }   // B, A
 
 // D[tmem of both CTAs] (+)= (A * scales) (B * scales)^T, M = 256 over the pair.
 __device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -52,13 +41,6 @@ __device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, 
 // repeated in the four lane quarters; each CTA of the pair copies its own.
 __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
-// Shared-memory descriptor of those 512 bytes: no swizzle, 8-row core matrices of
-// 16-byte rows, 128 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
-         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
 // --------------------------------------------------------------- shape of the kernel
@@ -96,35 +78,12 @@ __device__ __forceinline__ Unit unit_at(const GemmFp8Params& p, int u) {
   const int h = u - nfull, tile = h < 0 ? u : nfull + (h >> 1);
   Unit t{(tile / p.tiles_n) * 256, (tile % p.tiles_n) * 256, 256};
   if (h >= 0) { t.n0 += (h & 1) * 128; t.width = 128; }
-  if (p.N - t.n0 <= 128) t.width = 128;
+  if (p.N - t.n0 <= 128) t.width = 128;   // also where n0 >= N: such a half loads zeros and stores nothing
   return t;
-}
-
-// Word of scales (blocks 4 g .. 4 g + 3) of a row; rows outside the matrix scale by 1.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int pitch, int row, int rows, int g) {
-  return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(s + (int64_t)row * pitch) + g) : kUnitScale;
 }
 
 // Four values from the warp's copy of the bias (all lanes the same address: a broadcast).
 __device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
-// GELU for an e4m3 result, on packed pairs: max(x, 0) - |x| 2^G(|x|) as gelu_fast2, with
-// G = log2 Phi(-a) from a minimax polynomial of degree 5 over [0, 5.5] (relative error of the
-// result there at most 2.5e-4, a 250th of half an e4m3 step). Beyond, the polynomial keeps
-// falling, so no clamp is needed: the result is within 1.9e-8 |x| of max(x, 0), as GELU is.
-__device__ __forceinline__ void gelu_e4m3_2(float& x0, float& x1) {
-  constexpr float c0 = -1.000359058380127f, c1 = -1.1462607383728027f, c2 = -0.4696812331676483f,
-                  c3 = -0.04459895193576813f, c4 = 0.004869762342423201f, c5 = -0.00023325053916778415f;
-  const float a0 = fabsf(x0), a1 = fabsf(x1);
-  float g0, g1;
-  fma2(g0, g1, c5, c5, a0, a1, c4, c4);
-  fma2(g0, g1, g0, g1, a0, a1, c3, c3);
-  fma2(g0, g1, g0, g1, a0, a1, c2, c2);
-  fma2(g0, g1, g0, g1, a0, a1, c1, c1);
-  fma2(g0, g1, g0, g1, a0, a1, c0, c0);
-  x0 = fmaf(-a0, ex2(g0), fmaxf(x0, 0.f));
-  x1 = fmaf(-a1, ex2(g1), fmaxf(x1, 0.f));
-}
 
 template <bool kGelu, bool kE4m3, int n>
 __device__ __forceinline__ void bias_act(float (&t)[n], const float* bias) {
@@ -311,14 +270,17 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       for (int u = cluster; ok && u < units; u += nclusters) {
         const Unit t = unit_at(p, u);
         const int m0 = t.m0 + 128 * static_cast<int>(rank);
-        // a 128-wide unit uses the first 64 rows of each CTA's box (the rest is loaded and unused)
+        // boxes of 64 rows of W: two for a full unit, one for a 128-wide one
         const int n0 = t.n0 + (t.width / 2) * static_cast<int>(rank);
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
-          if (leader) mbar_arrive_expect_tx(&full[stage], 4 * kOperandBytes);
+          if (leader)
+            mbar_arrive_expect_tx(&full[stage], 2 * kOperandBytes + static_cast<uint32_t>(t.width) * kBK);
           const uint32_t bar = peer_addr(&full[stage], 0);
           tma_load_2d_pair(sA + stage * kOperandBytes, &map_a, bar, kb * kBK, m0);
           tma_load_2d_pair(sW + stage * kOperandBytes, &map_w, bar, kb * kBK, n0);
+          if (t.width == 256)
+            tma_load_2d_pair(sW + stage * kOperandBytes + kOperandBytes / 2, &map_w, bar, kb * kBK, n0 + 64);
           armed |= 1u << stage;
           armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -556,11 +518,10 @@ cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cud
   const int ncl = max_clusters[dev & 63];
   p.tiles_n = (p.N + 255) / 256;
   p.num_tiles = ((p.M + 255) / 256) * p.tiles_n;
-  // a last wave that would run at most half full runs as two 128-wide halves per tile
-  // (not where the last column tile is narrow already)
+  // a last wave that would run at most half full runs as two 128-wide halves per tile (of a
+  // narrow last column tile the second half has no columns)
   const int tail = p.num_tiles % ncl;
-  const bool narrow = p.N - (p.tiles_n - 1) * 256 <= 128;
-  p.tail = (!narrow && 2 * tail <= ncl) ? tail : 0;
+  p.tail = 2 * tail <= ncl ? tail : 0;
   const int units = p.num_tiles + p.tail;
   const int clusters = units < ncl ? units : ncl;
   gemm_fp8_kernel<kEpi, kGelu><<<2 * clusters, kThreads, kSmemBytes, stream>>>(m.a, m.w, m.c, p);

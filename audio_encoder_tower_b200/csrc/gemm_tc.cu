@@ -737,12 +737,12 @@ bool make_tma_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_fp8_operand_map(CUtensorMap* map, const void* q, int rows, int cols) {
+bool make_fp8_operand_map(CUtensorMap* map, const void* q, int rows, int cols, int box_rows) {
   auto fn = encode_fn();
   if (!fn || !q || (reinterpret_cast<uintptr_t>(q) & 15u) || (cols & 15)) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)cols};
-  cuuint32_t box[2] = {128, 128};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

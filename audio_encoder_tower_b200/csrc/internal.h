@@ -113,15 +113,25 @@ struct GemmFp8Params {
   int out_pitch;
   int* status;
 };
-// Operands (128 x 128 byte boxes) and output (32 rows of 128 bytes), 128-byte swizzle.
+// Operands (box_rows x 128 byte boxes; 128 rows of a and 64 of w in the 256 x 256 kernel)
+// and output (32 rows of 128 bytes), 128-byte swizzle.
 struct GemmFp8Maps {
   CUtensorMap a, w, c;
 };
 // e4m3 [rows, cols] operand; out_kind's [rows, cols] output.
-bool make_fp8_operand_map(CUtensorMap* map, const void* q, int rows, int cols);
+bool make_fp8_operand_map(CUtensorMap* map, const void* q, int rows, int cols, int box_rows);
 bool make_fp8_out_map(CUtensorMap* map, const void* out, int out_kind, int rows, int cols);
 cudaError_t launch_gemm_fp8(const GemmFp8Maps& m, const GemmFp8Params& p, int out_kind, int sm_count,
                             cudaStream_t stream);
+// The variant for few rows of A (gemm_fp8_small.cu): the plan for a shape, with tile_m == 0
+// where the 256 x 256 kernel is used. The map of A has boxes of tile_m rows.
+struct GemmFp8SmallPlan {
+  int tile_m;   // rows of A per CTA: 16, 32 or 64
+  int split;    // CTAs (a cluster) that share one tile's K
+};
+GemmFp8SmallPlan plan_gemm_fp8_small(int M, int N, int K, int sm_count);
+cudaError_t launch_gemm_fp8_small(const CUtensorMap& map_a, const CUtensorMap& map_w, const GemmFp8SmallPlan& plan,
+                                  const GemmFp8Params& p, void* out, int out_kind, cudaStream_t stream);
 cudaError_t launch_quantize_fp8(const void* x, bool x_bf16, int64_t ldx, int rows, int cols, uint8_t* q,
                                 uint8_t* scales, cudaStream_t s);
 cudaError_t launch_norm_fp8(int kind, const void* x, bool x_bf16, int64_t ldx, const void* delta, bool delta_bf16,
