@@ -26,7 +26,7 @@ EXPORTED = ["enc_create", "enc_forward", "enc_output_positions", "enc_get_status
             "enc_cache_create", "enc_forward_cached", "enc_cache_size", "enc_cache_destroy", "enc_cache_content_keys",
             "enc_clip_flops", "enc_shard_plan", "enc_selftest_timeout", "enc_check_guards",
             "enc_guard_selftest", "enc_fp8_scale_pitch", "enc_quantize_fp8", "enc_norm_fp8", "enc_linear_fp8"]
-ENC_FLAG_GUARD = 1
+ENC_FLAG_GUARD, ENC_FLAG_FP8 = 1, 2
 ENC_NORM_RMS, ENC_NORM_LAYER = 0, 1
 ENC_FP8_OUT_BF16, ENC_FP8_OUT_FP32, ENC_FP8_OUT_FP8, ENC_FP8_OUT_RESID = range(4)
 
@@ -171,11 +171,12 @@ def _stream_handle(stream) -> int | None:
 
 def encoder_config(*, n_mels, d_model, n_layers, n_heads, ffn_dim, max_frames, max_batch, dtype="bf16",
                    pool_step=1, proj_hidden=0, proj_out=0, ln_eps=1e-5, head_dim=64, attn_chunk=0,
-                   guard=False) -> EncConfig:
-    """The enc_config struct of a tower geometry (dtype "bf16" or "fp32"); guard sets ENC_FLAG_GUARD."""
+                   guard=False, fp8=False) -> EncConfig:
+    """The enc_config struct of a tower geometry (dtype "bf16" or "fp32"); guard sets
+    ENC_FLAG_GUARD, fp8 sets ENC_FLAG_FP8 (the blocks' linear layers in e4m3; dtype "bf16")."""
     return EncConfig(n_mels, d_model, n_layers, n_heads, head_dim, ffn_dim, max_frames, max_batch, pool_step,
                      proj_hidden, proj_out, ln_eps, ENC_DTYPE_BF16 if dtype == "bf16" else ENC_DTYPE_FP32,
-                     ENC_FLAG_GUARD if guard else 0, attn_chunk)
+                     (ENC_FLAG_GUARD if guard else 0) | (ENC_FLAG_FP8 if fp8 else 0), attn_chunk)
 
 
 def clip_flops(cfg: EncConfig, length: int) -> float:
@@ -214,16 +215,17 @@ class Encoder:
     weights: dict of device tensors in PyTorch layouts named as in enc.h
     ("conv1_w", "layers.{l}.q_w", "lnpost_g", "proj1_w", ...), dtype matching
     `dtype` ("bf16" or "fp32"). They may be freed after construction.
+    fp8=True runs the blocks' linear layers on e4m3 operands (ENC_FLAG_FP8).
     """
 
     def __init__(self, *, n_mels, d_model, n_layers, n_heads, ffn_dim, max_frames, max_batch, dtype="bf16",
                  pool_step=1, proj_hidden=0, proj_out=0, ln_eps=1e-5, head_dim=64, attn_chunk=0, guard=False,
-                 weights: dict):
+                 fp8=False, weights: dict):
         self.lib = load_library()
         self.cfg = encoder_config(n_mels=n_mels, d_model=d_model, n_layers=n_layers, n_heads=n_heads,
                                   ffn_dim=ffn_dim, max_frames=max_frames, max_batch=max_batch, dtype=dtype,
                                   pool_step=pool_step, proj_hidden=proj_hidden, proj_out=proj_out, ln_eps=ln_eps,
-                                  head_dim=head_dim, attn_chunk=attn_chunk, guard=guard)
+                                  head_dim=head_dim, attn_chunk=attn_chunk, guard=guard, fp8=fp8)
         w = EncWeights()
         for f in ("conv1_w", "conv1_b", "conv2_w", "conv2_b", "lnpost_g", "lnpost_b",
                   "proj1_w", "proj1_b", "proj2_w", "proj2_b"):

@@ -11,6 +11,7 @@
 #include "../../include/enc.h"
 #include "../../include/enc_profile.h"
 #include "common.cuh"
+#include "fp8.cuh"
 #include "internal.h"
 
 using namespace enc;
@@ -24,12 +25,21 @@ struct LayerMaps {
   CUtensorMap qkv, o, fc1, fc2;
 };
 
+// e4m3 rows with block scales (ENC_FLAG_FP8)
+struct Fp8Rows {
+  uint8_t *q = nullptr, *scales = nullptr;
+};
+struct LayerFp8 {
+  Fp8Rows qkv, o, fc1, fc2;
+};
+
 }  // namespace
 
 struct enc_handle {
   enc_config cfg;
   int device = 0, sm_count = 0;
   bool bf16 = true;
+  bool fp8 = false;          // ENC_FLAG_FP8: the blocks' linear layers in e4m3
   size_t esz = 2;            // bytes per element of cfg.dtype
   // geometry
   int T = 0, Tp = 0, P = 0, P1 = 0, p_out = 0, d_out = 0, mpad = 0;
@@ -49,6 +59,7 @@ struct enc_handle {
   void* conv2_w = nullptr;   // [d, 3, d]
   float *conv1_b = nullptr, *conv2_b = nullptr, *pe = nullptr;
   std::vector<void*> qkv_w, o_w, fc1_w, fc2_w;                 // per layer
+  std::vector<LayerFp8> w8;                                    // per layer, instead of those four
   std::vector<float*> qkv_b, o_b, fc1_b, fc2_b, ln1_g, ln1_b, ln2_g, ln2_b;
   float *lnpost_g = nullptr, *lnpost_b = nullptr;
   void *proj1_w = nullptr, *proj2_w = nullptr;
@@ -58,6 +69,7 @@ struct enc_handle {
   void* y1 = nullptr;        // [max_batch * Tp + 2, d]
   float* x = nullptr;        // [max_batch * P, d] residual stream
   void *a = nullptr, *qkv = nullptr, *o = nullptr, *f = nullptr, *e = nullptr, *p1 = nullptr;
+  Fp8Rows a8, o8, f8;        // ENC_FLAG_FP8: LN output, attention output, FFN hidden (instead of a and f)
   int* meta = nullptr;       // device [cu (B+1) | cu_out (B+1) | len (B) | cu_attn (segments+1)]
   int meta_ints = 0;         // capacity of meta / h_meta
   int* h_meta = nullptr;     // pinned host staging of meta
@@ -155,8 +167,9 @@ void free_all(enc_handle* h) {
 
 enc_status enc::validate_config(const enc_config* c) {
   if (!c) return ENC_ERR_INVALID_ARG;
-  if (c->flags & ~ENC_FLAG_GUARD) return ENC_ERR_INVALID_ARG;
+  if (c->flags & ~(ENC_FLAG_GUARD | ENC_FLAG_FP8)) return ENC_ERR_INVALID_ARG;
   if (c->dtype != ENC_DTYPE_BF16 && c->dtype != ENC_DTYPE_FP32) return ENC_ERR_INVALID_ARG;
+  if ((c->flags & ENC_FLAG_FP8) && c->dtype != ENC_DTYPE_BF16) return ENC_ERR_INVALID_ARG;
   if (c->n_mels <= 0 || c->d_model <= 0 || c->n_layers < 0 || c->n_heads <= 0 || c->ffn_dim <= 0 ||
       c->max_frames <= 0 || c->max_batch <= 0)
     return ENC_ERR_INVALID_ARG;
@@ -197,6 +210,32 @@ enc_status to_f32(enc_handle* h, const void* src, int n, float fill, float** dst
   return ENC_OK;
 }
 
+size_t fp8_scale_bytes(size_t rows, int cols) { return rows * (size_t)fp8_pitch(cols); }
+
+// Storage of an 8-bit weight, and rows row0 .. of it from a bf16 matrix [rows, cols]. The
+// quantisation reads 8 bytes at a time: a source with a lesser alignment goes through a copy.
+enc_status alloc_fp8_weight(enc_handle* h, int rows, int cols, Fp8Rows* w) {
+  ENC_CHECK(dev_alloc(h, &w->q, (size_t)rows * cols));
+  return dev_alloc(h, &w->scales, fp8_scale_bytes(rows, cols));
+}
+enc_status quantize_weight(const void* src, int rows, int cols, const Fp8Rows& w, int row0) {
+  void* copy = nullptr;
+  if (reinterpret_cast<uintptr_t>(src) & 7u) {
+    const size_t bytes = (size_t)rows * cols * 2;
+    ENC_TRY(cudaMalloc(&copy, bytes));
+    const cudaError_t e = cudaMemcpy(copy, src, bytes, cudaMemcpyDeviceToDevice);
+    if (e != cudaSuccess) {
+      cudaFree(copy);
+      return cuda_status(e);
+    }
+    src = copy;
+  }
+  const cudaError_t e = launch_quantize_fp8(src, true, cols, rows, cols, w.q + (size_t)row0 * cols,
+                                            w.scales + fp8_scale_bytes(row0, cols), 0);
+  if (copy) cudaFree(copy);   // waits for the kernel
+  return cuda_status(e);
+}
+
 bool map_rows(CUtensorMap* m, const void* base, int inner, long long rows, int box_rows) {
   return make_tma_2d(m, base, (uint64_t)inner, (uint64_t)rows, (uint64_t)inner * 2, 64, (uint32_t)box_rows);
 }
@@ -219,23 +258,38 @@ enc_status build(enc_handle* h, const enc_weights* w) {
   h->qkv_w.resize(L); h->o_w.resize(L); h->fc1_w.resize(L); h->fc2_w.resize(L);
   h->qkv_b.resize(L); h->o_b.resize(L); h->fc1_b.resize(L); h->fc2_b.resize(L);
   h->ln1_g.resize(L); h->ln1_b.resize(L); h->ln2_g.resize(L); h->ln2_b.resize(L);
+  if (h->fp8) h->w8.resize(L);
   const size_t dd = (size_t)d * d;
   for (int l = 0; l < L; ++l) {
     if (!w->q_w[l] || !w->k_w[l] || !w->v_w[l] || !w->o_w[l] || !w->fc1_w[l] || !w->fc2_w[l])
       return ENC_ERR_INVALID_ARG;
-    ENC_CHECK(dev_alloc(h, &h->qkv_w[l], 3 * dd * h->esz));
-    uint8_t* q = reinterpret_cast<uint8_t*>(h->qkv_w[l]);
-    ENC_TRY(cudaMemcpy(q, w->q_w[l], dd * h->esz, cudaMemcpyDeviceToDevice));
-    ENC_TRY(cudaMemcpy(q + dd * h->esz, w->k_w[l], dd * h->esz, cudaMemcpyDeviceToDevice));
-    ENC_TRY(cudaMemcpy(q + 2 * dd * h->esz, w->v_w[l], dd * h->esz, cudaMemcpyDeviceToDevice));
+    if (h->fp8) {
+      LayerFp8& w8 = h->w8[l];
+      ENC_CHECK(alloc_fp8_weight(h, 3 * d, d, &w8.qkv));
+      ENC_CHECK(quantize_weight(w->q_w[l], d, d, w8.qkv, 0));
+      ENC_CHECK(quantize_weight(w->k_w[l], d, d, w8.qkv, d));
+      ENC_CHECK(quantize_weight(w->v_w[l], d, d, w8.qkv, 2 * d));
+      ENC_CHECK(alloc_fp8_weight(h, d, d, &w8.o));
+      ENC_CHECK(quantize_weight(w->o_w[l], d, d, w8.o, 0));
+      ENC_CHECK(alloc_fp8_weight(h, F, d, &w8.fc1));
+      ENC_CHECK(quantize_weight(w->fc1_w[l], F, d, w8.fc1, 0));
+      ENC_CHECK(alloc_fp8_weight(h, d, F, &w8.fc2));
+      ENC_CHECK(quantize_weight(w->fc2_w[l], d, F, w8.fc2, 0));
+    } else {
+      ENC_CHECK(dev_alloc(h, &h->qkv_w[l], 3 * dd * h->esz));
+      uint8_t* q = reinterpret_cast<uint8_t*>(h->qkv_w[l]);
+      ENC_TRY(cudaMemcpy(q, w->q_w[l], dd * h->esz, cudaMemcpyDeviceToDevice));
+      ENC_TRY(cudaMemcpy(q + dd * h->esz, w->k_w[l], dd * h->esz, cudaMemcpyDeviceToDevice));
+      ENC_TRY(cudaMemcpy(q + 2 * dd * h->esz, w->v_w[l], dd * h->esz, cudaMemcpyDeviceToDevice));
+      ENC_CHECK(copy_weight(h, w->o_w[l], dd, &h->o_w[l]));
+      ENC_CHECK(copy_weight(h, w->fc1_w[l], (size_t)F * d, &h->fc1_w[l]));
+      ENC_CHECK(copy_weight(h, w->fc2_w[l], (size_t)d * F, &h->fc2_w[l]));
+    }
     ENC_CHECK(dev_alloc(h, &h->qkv_b[l], 3 * (size_t)d * 4));
     ENC_TRY(launch_to_f32(w->q_b[l], h->bf16, h->qkv_b[l], d, 0.f, 0));
     // a key bias shifts every score of a query row equally and cancels in softmax: k runs unbiased
     ENC_TRY(launch_to_f32(nullptr, h->bf16, h->qkv_b[l] + d, d, 0.f, 0));
     ENC_TRY(launch_to_f32(w->v_b[l], h->bf16, h->qkv_b[l] + 2 * d, d, 0.f, 0));
-    ENC_CHECK(copy_weight(h, w->o_w[l], dd, &h->o_w[l]));
-    ENC_CHECK(copy_weight(h, w->fc1_w[l], (size_t)F * d, &h->fc1_w[l]));
-    ENC_CHECK(copy_weight(h, w->fc2_w[l], (size_t)d * F, &h->fc2_w[l]));
     ENC_CHECK(to_f32(h, w->o_b[l], d, 0.f, &h->o_b[l]));
     ENC_CHECK(to_f32(h, w->fc1_b[l], F, 0.f, &h->fc1_b[l]));
     ENC_CHECK(to_f32(h, w->fc2_b[l], d, 0.f, &h->fc2_b[l]));
@@ -263,19 +317,28 @@ enc_status build(enc_handle* h, const enc_weights* w) {
   ENC_TRY(cudaMemset(h->melT, 0, (size_t)(rows_t + 2) * M * h->esz));
   ENC_TRY(cudaMemset(h->y1, 0, (size_t)(rows_t + 2) * d * h->esz));
   ENC_CHECK(ws_alloc(h, &h->x, (size_t)rows_p * d * 4, "x"));
-  ENC_CHECK(ws_alloc(h, &h->a, (size_t)rows_p * d * h->esz, "a"));
+  if (h->fp8) {
+    ENC_CHECK(ws_alloc(h, &h->a8.q, (size_t)rows_p * d, "a8"));
+    ENC_CHECK(ws_alloc(h, &h->a8.scales, fp8_scale_bytes(rows_p, d), "a8 scales"));
+    ENC_CHECK(ws_alloc(h, &h->o8.q, (size_t)rows_p * d, "o8"));
+    ENC_CHECK(ws_alloc(h, &h->o8.scales, fp8_scale_bytes(rows_p, d), "o8 scales"));
+    ENC_CHECK(ws_alloc(h, &h->f8.q, (size_t)rows_p * F, "f8"));
+    ENC_CHECK(ws_alloc(h, &h->f8.scales, fp8_scale_bytes(rows_p, F), "f8 scales"));
+  } else {
+    ENC_CHECK(ws_alloc(h, &h->a, (size_t)rows_p * d * h->esz, "a"));
+  }
   ENC_CHECK(ws_alloc(h, &h->qkv, (size_t)rows_p * 3 * d * h->esz, "qkv"));
   ENC_CHECK(ws_alloc(h, &h->o, (size_t)rows_p * d * h->esz, "o"));
-  ENC_CHECK(ws_alloc(h, &h->f, (size_t)rows_p * F * h->esz, "f"));
+  if (!h->fp8) ENC_CHECK(ws_alloc(h, &h->f, (size_t)rows_p * F * h->esz, "f"));
   if (ph) {
     ENC_CHECK(ws_alloc(h, &h->e, (size_t)rows_o * d * h->esz, "e"));
     ENC_CHECK(ws_alloc(h, &h->p1, (size_t)rows_o * ph * h->esz, "p1"));
   }
   ENC_TRY(cudaMemset(h->x, 0, (size_t)rows_p * d * 4));
-  ENC_TRY(cudaMemset(h->a, 0, (size_t)rows_p * d * h->esz));
+  if (!h->fp8) ENC_TRY(cudaMemset(h->a, 0, (size_t)rows_p * d * h->esz));
   ENC_TRY(cudaMemset(h->qkv, 0, (size_t)rows_p * 3 * d * h->esz));
   ENC_TRY(cudaMemset(h->o, 0, (size_t)rows_p * d * h->esz));
-  ENC_TRY(cudaMemset(h->f, 0, (size_t)rows_p * F * h->esz));
+  if (!h->fp8) ENC_TRY(cudaMemset(h->f, 0, (size_t)rows_p * F * h->esz));
   // block-local attention adds the chunk boundaries: at most ceil(P / chunk) per clip
   h->meta_ints = 3 * Bm + 2 + (c.attn_chunk > 0 ? Bm * ((h->P + c.attn_chunk - 1) / c.attn_chunk) + 1 : 0);
   ENC_CHECK(ws_alloc(h, &h->meta, (size_t)h->meta_ints * 4, "meta"));
@@ -292,14 +355,16 @@ enc_status build(enc_handle* h, const enc_weights* w) {
     const uint8_t* melT_data = reinterpret_cast<const uint8_t*>(h->melT) + (size_t)M * 2;
     bool ok = map_rows(&h->m_conv1_a, melT_data, M, rows_t, 128);
     ok = ok && make_tma_2d(&h->m_conv2_a, h->y1, 2 * (uint64_t)d, (uint64_t)rows_t / 2, 4 * (uint64_t)d, 64, 128);
-    ok = ok && map_rows(&h->m_a, h->a, d, rows_p, 128);
-    ok = ok && map_rows(&h->m_o, h->o, d, rows_p, 128);
-    ok = ok && map_rows(&h->m_f, h->f, F, rows_p, 128);
+    if (!h->fp8) {
+      ok = ok && map_rows(&h->m_a, h->a, d, rows_p, 128);
+      ok = ok && map_rows(&h->m_o, h->o, d, rows_p, 128);
+      ok = ok && map_rows(&h->m_f, h->f, F, rows_p, 128);
+      ok = ok && make_out_map(&h->m_out_f, h->f, (uint64_t)rows_p, (uint64_t)F);
+    }
     ok = ok && make_qkv_maps(&h->m_qkv, h->qkv, (int)rows_p, d);
     ok = ok && make_resid_map(&h->m_x, h->x, (uint64_t)rows_p, (uint64_t)d);
     ok = ok && make_out_map(&h->m_out_y1, h->y1, (uint64_t)rows_t, (uint64_t)d);
     ok = ok && make_out_map(&h->m_out_qkv, h->qkv, (uint64_t)rows_p, 3 * (uint64_t)d);
-    ok = ok && make_out_map(&h->m_out_f, h->f, (uint64_t)rows_p, (uint64_t)F);
     ok = ok && map_rows(&h->m_conv1_w, h->conv1_w, 3 * h->mpad, d, 128);
     ok = ok && map_rows(&h->m_conv2_w, h->conv2_w, 3 * d, d, 128);
     if (ph) {
@@ -311,6 +376,14 @@ enc_status build(enc_handle* h, const enc_weights* w) {
     }
     h->lmaps.resize(L);
     for (int l = 0; ok && l < L; ++l) {
+      if (h->fp8) {
+        const LayerFp8& w8 = h->w8[l];
+        ok = ok && make_fp8_operand_map(&h->lmaps[l].qkv, w8.qkv.q, 3 * d, d, 64);
+        ok = ok && make_fp8_operand_map(&h->lmaps[l].o, w8.o.q, d, d, 64);
+        ok = ok && make_fp8_operand_map(&h->lmaps[l].fc1, w8.fc1.q, F, d, 64);
+        ok = ok && make_fp8_operand_map(&h->lmaps[l].fc2, w8.fc2.q, d, F, 64);
+        continue;
+      }
       ok = ok && map_rows(&h->lmaps[l].qkv, h->qkv_w[l], d, 3 * d, 128);
       ok = ok && map_rows(&h->lmaps[l].o, h->o_w[l], d, d, 128);
       ok = ok && map_rows(&h->lmaps[l].fc1, h->fc1_w[l], d, F, 128);
@@ -430,6 +503,57 @@ int stage_meta(const enc_handle* h, const int32_t* lengths, int B, int* hm, Work
   return total;
 }
 
+// The encoder blocks with their linear layers in e4m3 (ENC_FLAG_FP8). Every product runs on the
+// 256 x 256 kernel, also for few rows: its sums do not depend on the number of rows, so a clip's
+// output does not depend on its batch. The maps of the activations end at this batch's rows.
+enc_status blocks_fp8(enc_handle* h, const Work& wk, const int* cu_att, cudaStream_t s) {
+  const enc_config& c = h->cfg;
+  const int d = c.d_model, F = c.ffn_dim, R = wk.R;
+  const double Rd = (double)R * d;
+  CUtensorMap ma, mo, mf, out_qkv, out_x, out_f;
+  if (!make_fp8_operand_map(&ma, h->a8.q, R, d, 128) || !make_fp8_operand_map(&mo, h->o8.q, R, d, 128) ||
+      !make_fp8_operand_map(&mf, h->f8.q, R, F, 128) ||
+      !make_fp8_out_map(&out_qkv, h->qkv, ENC_FP8_OUT_BF16, R, 3 * d) ||
+      !make_fp8_out_map(&out_x, h->x, ENC_FP8_OUT_RESID, R, d) ||
+      !make_fp8_out_map(&out_f, h->f8.q, ENC_FP8_OUT_FP8, R, F))
+    return ENC_ERR_CUDA;
+  auto linear = [&](const CUtensorMap& a, const Fp8Rows& ar, const CUtensorMap& w, const Fp8Rows& wr,
+                    const CUtensorMap& out, const float* bias, int N, int K, int kind, uint8_t* out_scales) {
+    GemmFp8Params p;
+    memset(&p, 0, sizeof(p));
+    p.M = R; p.N = N; p.num_kb = fp8_blocks(K);
+    p.a_scales = ar.scales; p.w_scales = wr.scales; p.k_pitch = fp8_pitch(K);
+    p.bias = bias;
+    p.gelu = kind == ENC_FP8_OUT_FP8;
+    p.out_scales = out_scales; p.out_pitch = fp8_pitch(N);
+    p.status = h->status;
+    return launch_gemm_fp8({a, w, out}, p, kind, h->sm_count, s);
+  };
+  auto norm = [&](const float* g, const float* b) {
+    return launch_norm_fp8(ENC_NORM_LAYER, h->x, false, d, nullptr, false, d, g, b, c.ln_eps, R, d, nullptr, d,
+                           h->a8.q, h->a8.scales, s);
+  };
+  for (int l = 0; l < c.n_layers; ++l) {
+    Range block("encoder block");
+    const LayerMaps& lm = h->lmaps[l];
+    const LayerFp8& w = h->w8[l];
+    ENC_RUN(ENC_K_LN, 0.0, norm(h->ln1_g[l], h->ln1_b[l]));
+    ENC_RUN(ENC_K_QKV, 6.0 * Rd * d,
+            linear(ma, h->a8, lm.qkv, w.qkv, out_qkv, h->qkv_b[l], 3 * d, d, ENC_FP8_OUT_BF16, nullptr));
+    ENC_RUN(ENC_K_ATTN, 4.0 * wk.sum_seg2 * d,
+            launch_attention_tc(h->m_qkv, reinterpret_cast<bf16*>(h->o), cu_att, wk.nseg, wk.max_seg, d, c.n_heads,
+                                h->status, s));
+    ENC_RUN(ENC_K_OUT, 0.0, launch_quantize_fp8(h->o, true, d, R, d, h->o8.q, h->o8.scales, s));
+    ENC_RUN(ENC_K_OUT, 2.0 * Rd * d, linear(mo, h->o8, lm.o, w.o, out_x, h->o_b[l], d, d, ENC_FP8_OUT_RESID, nullptr));
+    ENC_RUN(ENC_K_LN, 0.0, norm(h->ln2_g[l], h->ln2_b[l]));
+    ENC_RUN(ENC_K_FC1, 2.0 * Rd * F,
+            linear(ma, h->a8, lm.fc1, w.fc1, out_f, h->fc1_b[l], F, d, ENC_FP8_OUT_FP8, h->f8.scales));
+    ENC_RUN(ENC_K_FC2, 2.0 * Rd * F,
+            linear(mf, h->f8, lm.fc2, w.fc2, out_x, h->fc2_b[l], d, F, ENC_FP8_OUT_RESID, nullptr));
+  }
+  return ENC_OK;
+}
+
 enc_status forward_bf16(enc_handle* h, const void* mel, void* out, const Work& wk, cudaStream_t s) {
   const enc_config& c = h->cfg;
   const int d = c.d_model, F = c.ffn_dim, M = c.n_mels, B = wk.B, R = wk.R;
@@ -458,7 +582,8 @@ enc_status forward_bf16(enc_handle* h, const void* mel, void* out, const Work& w
   ENC_RUN(ENC_K_CONV2, 2.0 * Rd * 3 * d, launch_gemm_tc(h->m_conv2_a, h->m_conv2_w, g, h->sm_count, s));
 
   bf16* a = reinterpret_cast<bf16*>(h->a);
-  for (int l = 0; l < c.n_layers; ++l) {
+  if (h->fp8) ENC_CHECK(blocks_fp8(h, wk, cu_att, s));
+  for (int l = 0; l < (h->fp8 ? 0 : c.n_layers); ++l) {
     Range block("encoder block");
     const LayerMaps& lm = h->lmaps[l];
     ENC_RUN(ENC_K_LN, 0.0, launch_layernorm<bf16>(h->x, h->ln1_g[l], h->ln1_b[l], a, R, d, c.ln_eps, s));
@@ -647,6 +772,7 @@ enc_status enc_create(const enc_config* cfg, const enc_weights* w, enc_handle** 
   h->device = dev;
   h->sm_count = prop.multiProcessorCount;
   h->bf16 = cfg->dtype == ENC_DTYPE_BF16;
+  h->fp8 = (cfg->flags & ENC_FLAG_FP8) != 0;
   h->esz = h->bf16 ? 2 : 4;
   h->T = cfg->max_frames;
   h->Tp = round_up(h->T + 2, 2);
@@ -864,10 +990,16 @@ extern "C" enc_status enc_forward_static_scratch(enc_handle* h, const void* mel,
   unsigned char* melT = take((rows_t + 2) * M * h->esz);
   unsigned char* y1 = take((rows_t + 2) * d * h->esz);
   unsigned char* x = take((size_t)R * d * 4);
-  unsigned char* a = take((size_t)R * d * h->esz);
+  unsigned char* a = h->fp8 ? nullptr : take((size_t)R * d * h->esz);
   unsigned char* qkv = take((size_t)R * 3 * d * h->esz);
   unsigned char* o = take((size_t)R * d * h->esz);
-  unsigned char* f = take((size_t)R * F * h->esz);
+  unsigned char* f = h->fp8 ? nullptr : take((size_t)R * F * h->esz);
+  Fp8Rows a8, o8, f8;
+  if (h->fp8) {
+    a8 = {take((size_t)R * d), take(fp8_scale_bytes(R, d))};
+    o8 = {take((size_t)R * d), take(fp8_scale_bytes(R, d))};
+    f8 = {take((size_t)R * F), take(fp8_scale_bytes(R, F))};
+  }
   unsigned char* e = c.proj_hidden ? take((size_t)R_out * d * h->esz) : nullptr;
   unsigned char* p1 = c.proj_hidden ? take((size_t)R_out * c.proj_hidden * h->esz) : nullptr;
   unsigned char* meta = take((size_t)nints * 4);
@@ -887,22 +1019,26 @@ extern "C" enc_status enc_forward_static_scratch(enc_handle* h, const void* mel,
                     s_mf = h->m_f, s_me = h->m_e, s_mp1 = h->m_p1, s_mx = h->m_x;
   const QkvMaps s_mqkv = h->m_qkv;
   const CUtensorMap s_oy1 = h->m_out_y1, s_oqkv = h->m_out_qkv, s_of = h->m_out_f, s_op1 = h->m_out_p1;
+  const Fp8Rows s_a8 = h->a8, s_o8 = h->o8, s_f8 = h->f8;
   const bool s_profile = h->profile;
   h->melT = melT; h->y1 = y1; h->x = reinterpret_cast<float*>(x); h->a = a; h->qkv = qkv; h->o = o; h->f = f;
   h->e = e; h->p1 = p1; h->meta = reinterpret_cast<int*>(meta);
+  h->a8 = a8; h->o8 = o8; h->f8 = f8;
   h->profile = false;   // event records would grow host-side lists
   st = ENC_OK;
   if (h->bf16) {
     bool ok = map_rows(&h->m_conv1_a, melT + (size_t)M * 2, M, (long long)rows_t, 128);
     ok = ok && make_tma_2d(&h->m_conv2_a, y1, 2 * (uint64_t)d, (uint64_t)rows_t / 2, 4 * (uint64_t)d, 64, 128);
-    ok = ok && map_rows(&h->m_a, a, d, R, 128);
-    ok = ok && map_rows(&h->m_o, o, d, R, 128);
-    ok = ok && map_rows(&h->m_f, f, F, R, 128);
+    if (!h->fp8) {
+      ok = ok && map_rows(&h->m_a, a, d, R, 128);
+      ok = ok && map_rows(&h->m_o, o, d, R, 128);
+      ok = ok && map_rows(&h->m_f, f, F, R, 128);
+      ok = ok && make_out_map(&h->m_out_f, f, (uint64_t)R, (uint64_t)F);
+    }
     ok = ok && make_qkv_maps(&h->m_qkv, qkv, R, d);
     ok = ok && make_resid_map(&h->m_x, reinterpret_cast<float*>(x), (uint64_t)R, (uint64_t)d);
     ok = ok && make_out_map(&h->m_out_y1, y1, (uint64_t)rows_t, (uint64_t)d);
     ok = ok && make_out_map(&h->m_out_qkv, qkv, (uint64_t)R, 3 * (uint64_t)d);
-    ok = ok && make_out_map(&h->m_out_f, f, (uint64_t)R, (uint64_t)F);
     if (c.proj_hidden) {
       ok = ok && map_rows(&h->m_e, e, d, R_out > 0 ? R_out : 1, 128);
       ok = ok && map_rows(&h->m_p1, p1, c.proj_hidden, R_out > 0 ? R_out : 1, 128);
@@ -921,6 +1057,7 @@ extern "C" enc_status enc_forward_static_scratch(enc_handle* h, const void* mel,
   }
   h->melT = s_melT; h->y1 = s_y1; h->x = s_x; h->a = s_a; h->qkv = s_qkv; h->o = s_o; h->f = s_f; h->e = s_e;
   h->p1 = s_p1; h->meta = s_meta;
+  h->a8 = s_a8; h->o8 = s_o8; h->f8 = s_f8;
   h->m_conv1_a = s_conv1_a; h->m_conv2_a = s_conv2_a; h->m_a = s_ma; h->m_o = s_mo; h->m_f = s_mf; h->m_e = s_me;
   h->m_p1 = s_mp1;
   h->m_qkv = s_mqkv;

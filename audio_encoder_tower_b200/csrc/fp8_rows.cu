@@ -206,7 +206,9 @@ norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
   constexpr int kRagged = 2;
   constexpr int kStep = WPR * kFp8Block;     // columns from one of a warp's blocks to its next
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = (int64_t)blockIdx.x * (kWarps / WPR) + warp / WPR;
+  // rows from the last to the first: a product that updated x just before, tiles in ascending
+  // order, has left the last rows in L2, and the next product reads the first rows first
+  const int64_t row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * (kWarps / WPR) + warp / WPR;
   const bool live = row0 < p.rows;           // all warps stay for the block's barriers
   const int64_t row = live ? row0 : 0;
   const int part = warp % WPR;

@@ -509,8 +509,12 @@ def main():
     ap.add_argument("--kernel", choices=["qkv", "out", "fc1", "fc2", "attention", "frontend", "cache", "sidestream",
                                         "block"],
                     help="time one layer kernel of the workload alone (profiling aid)")
+    ap.add_argument("--fp8", action="store_true",
+                    help="the blocks' linear layers on e4m3 operands (not the default workload's precision)")
     args = ap.parse_args()
     cfg = S.CONFIGS[args.config]
+    if args.fp8 and (args.kernel or args.impl != "ours"):
+        ap.error("--fp8 times the whole forward of this library")
     if args.kernel == "sidestream":
         return run_sidestream(args, cfg)
     if args.kernel:
@@ -546,7 +550,7 @@ def main():
     enc = Encoder(n_mels=cfg.n_mels, d_model=cfg.d_model, n_layers=cfg.n_layers, n_heads=cfg.n_heads,
                   ffn_dim=cfg.ffn_dim, max_frames=cfg.frames, max_batch=cfg.batch, dtype=cfg.dtype,
                   pool_step=cfg.pool_step, proj_hidden=cfg.proj_hidden, proj_out=cfg.proj_out,
-                  attn_chunk=cfg.attn_chunk, weights=w_dev)
+                  attn_chunk=cfg.attn_chunk, fp8=args.fp8, weights=w_dev)
     del w_dev
     torch.cuda.empty_cache()
     mel = torch.from_numpy(mel_np).to(device=dev, dtype=dt)
@@ -653,12 +657,14 @@ def main():
     peak_tf = float(peaks.get("bf16_tflops_sustained", FALLBACK_PEAKS["bf16_tflops_sustained"]))
     ach = (g_fl / g_n) / (g_ms / g_n) / 1e9 if g_n else 0.0
     traffic = gemm_traffic_record()
-    roofline = {"kernel": ("tcgen05 GEMM: gemm_tc2_kernel on SM pairs where N % 256 == 0 (every GEMM of the "
+    roofline = {"kernel": ("gemm_fp8_kernel (with the quantisation before the output projection); conv and projector "
+                           "on gemm_tc2_kernel; all GEMM launches of the timed region") if args.fp8 else
+                          ("tcgen05 GEMM: gemm_tc2_kernel on SM pairs where N % 256 == 0 (every GEMM of the "
                            "Whisper workloads), else gemm_tc_kernel; all GEMM launches of the timed region"),
                 "bound": "tensor", "achieved": ach, "peak": peak_tf, "unit": "TFLOP/s", "frac": ach / peak_tf,
                 "peak_source": f"{peak_src} bf16_tflops_sustained (kernel timed inside a long step)",
                 "frac_of_burst_peak": ach / float(peaks.get("bf16_tflops", FALLBACK_PEAKS["bf16_tflops"])),
-                "traffic": (traffic["bytes_per_launch"] if traffic else None),
+                "traffic": (traffic["bytes_per_launch"] if traffic and not args.fp8 else None),
                 "share_of_step": g_ms / step_ms_prof if step_ms_prof else None,
                 "launches": g_n, "flops_per_launch": g_fl / g_n if g_n else None}
     kernels = {k: {"ms_per_step": v[0] / args.steps, "tflops": (v[1] / v[0] / 1e9 if v[0] and v[1] else None),
@@ -667,7 +673,8 @@ def main():
     tflops = flops_job / world / ms / 1e9     # per GPU
     line = {"metric": METRIC, "value": job_throughput(audio_s_job, ms), "unit": UNIT, "n_gpus": world,
             "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
-            "scaling": "weak", "vs_baseline": None, "dtype": cfg.dtype, "data": "synthetic (seeded; random weights)",
+            "scaling": "weak", "vs_baseline": None, "dtype": cfg.dtype + (" with e4m3 linear layers" if args.fp8 else ""),
+            "data": "synthetic (seeded; random weights)",
             "config": workload_desc(cfg, world),
             "tflops": world * tflops,
             "frac_bf16_peak": tflops / float(peaks.get("bf16_tflops", FALLBACK_PEAKS["bf16_tflops"])),

@@ -78,6 +78,20 @@ typedef enum enc_status {
  */
 #define ENC_FLAG_GUARD 1u
 
+/*
+ * enc_config.flags: ENC_FLAG_FP8 runs the linear layers of the encoder blocks
+ * (q/k/v, output projection, fc1, fc2) on e4m3 operands with a power-of-two scale
+ * for each block of 128 elements along K (enc_fp8.h). enc_create quantises the
+ * weights; the LayerNorms write e4m3, fc1's epilogue quantises the GELU output,
+ * and the attention output is quantised before the output projection. The conv
+ * stem, attention, residual stream (fp32), final LayerNorm and projector are as
+ * without the flag. dtype must be ENC_DTYPE_BF16: weights, mel and out are bf16.
+ * Against the exact result the output is seven to ten times as far as in bf16 (e4m3
+ * holds 4 significant bits, bf16 holds 8): 1.2 to 1.8 % of its norm instead of 0.18 %
+ * on a two-block tower with N(0, 0.02) weights.
+ */
+#define ENC_FLAG_FP8 2u
+
 typedef enum enc_dtype {
   ENC_DTYPE_BF16 = 0,
   ENC_DTYPE_FP32 = 1
@@ -98,7 +112,7 @@ typedef struct enc_config {
   int32_t proj_out;      /* projector output width (multiple of 128) */
   float ln_eps;          /* LayerNorm epsilon (1e-5) */
   int32_t dtype;         /* enc_dtype */
-  uint32_t flags;        /* 0, or ENC_FLAG_GUARD; other bits are reserved and rejected */
+  uint32_t flags;        /* ENC_FLAG_* bits; other bits are reserved and rejected */
   int32_t attn_chunk;    /* 0: full bidirectional attention within each clip; > 0: block-local
                             attention, position i of a clip attending only within its chunk of
                             attn_chunk positions (MiniCPM-o-2.6, "(2) AUDIO": audio_chunk_length

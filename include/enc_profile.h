@@ -24,7 +24,7 @@ typedef enum enc_kernel_class {
   ENC_K_LN = 3,      /* pre-attention / pre-FFN LayerNorm */
   ENC_K_QKV = 4,     /* fused q/k/v projection */
   ENC_K_ATTN = 5,    /* attention */
-  ENC_K_OUT = 6,     /* output projection + residual */
+  ENC_K_OUT = 6,     /* output projection + residual (ENC_FLAG_FP8: and the quantisation before it) */
   ENC_K_FC1 = 7,     /* FFN up-projection + GELU */
   ENC_K_FC2 = 8,     /* FFN down-projection + residual */
   ENC_K_FINAL = 9,   /* final LayerNorm (+ pool, + unpack) */
