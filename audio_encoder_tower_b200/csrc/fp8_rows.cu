@@ -200,15 +200,17 @@ template <int kDelta> struct DeltaType { using type = bf16; };
 template <> struct DeltaType<2> { using type = float; };
 
 template <typename T, int kDelta, int NV, int WPR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
 norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
   __shared__ float shared[kWarps];
   constexpr int kRagged = 2;
   constexpr int kStep = WPR * kFp8Block;     // columns from one of a warp's blocks to its next
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // rows from the last to the first: a product that updated x just before, tiles in ascending
-  // order, has left the last rows in L2, and the next product reads the first rows first
-  const int64_t row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * (kWarps / WPR) + warp / WPR;
+  // Without a delta, rows from the last to the first: a product that updated x just before, tiles
+  // in ascending order, has left the last rows in L2, and the next product reads the first rows
+  // first (the encoder's norms 35.3 -> 33.8 us at 24000 x 1280). With one, upwards.
+  const int64_t block = kDelta == 0 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const int64_t row0 = block * (kWarps / WPR) + warp / WPR;
   const bool live = row0 < p.rows;           // all warps stay for the block's barriers
   const int64_t row = live ? row0 : 0;
   const int part = warp % WPR;
