@@ -43,11 +43,31 @@ __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sde
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// Whether the phase of `bar` with the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_peek(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 // --------------------------------------------------------------- shape of the kernel
 // A cluster of two CTAs computes 256 x 256 tiles (M = 256 over the pair). CTA r holds
 // rows 128 r .. of the A tile and rows 128 r .. of the W tile in a ring of 32 KB stages.
-//   warp 0   TMA producer;  warp 2  scales;  warp 3  none
-//   warp 1   first CTA: MMA issuer; second CTA: tells the first that its scales are written
+//   warp 0   TMA producer;  warp 1  (first CTA) MMA issuer;  warp 3  none
+//   warp 2   (first CTA) scales of both CTAs, the second's by stores over the cluster: so one
+//            fence and one arrival in the issuer's own CTA cover them (an arrival from the other
+//            CTA that releases its writes took 1,500 cycles)
 //   warps 4..  epilogue: warps of a TMEM lane quarter split the tile's columns
 // TMEM has 512 columns: two accumulators of 256 and the scales do not fit side by side.
 // The accumulators overlap instead, by 32 columns: 0..255 and 224..479, scales from
@@ -221,9 +241,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   float* sB = reinterpret_cast<float*>(sS + kScaleSlots * kScaleSlotBytes);   // bias, 128 columns per epilogue warp
   uint64_t* full = reinterpret_cast<uint64_t*>(sB + kEpiWarps * 128);         // used in the first CTA
   uint64_t* empty = full + kStages;
-  uint64_t* sfull = empty + kStages;        // [4] this CTA's scales are written
-  uint64_t* speer = sfull + kScaleSlots;    // [4] and the second CTA's; used in the first CTA
-  uint64_t* sempty = speer + kScaleSlots;   // [4] MMAs that read the slot are done
+  uint64_t* sfull = empty + kStages;        // [4] scales of both CTAs written; used in the first CTA
+  uint64_t* sempty = sfull + kScaleSlots;   // [4] MMAs that read the slot are done; used in the first CTA
   uint64_t* tfull = sempty + kScaleSlots;   // [2] accumulator complete
   uint64_t* tempty = tfull + 2;             // shared columns read; used in the first CTA
   uint64_t* drain = tempty + 1;
@@ -238,7 +257,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int s = 0; s < kScaleSlots; ++s) { mbar_init(&sfull[s], 1); mbar_init(&speer[s], 1); mbar_init(&sempty[s], 1); }
+    for (int s = 0; s < kScaleSlots; ++s) { mbar_init(&sfull[s], 1); mbar_init(&sempty[s], 1); }
     for (int a = 0; a < 2; ++a) mbar_init(&tfull[a], 1);
     mbar_init(tempty, 2 * kEpiWarps);
     mbar_init(drain, 1);
@@ -259,38 +278,38 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   const uint32_t tmem_base = *tmem_slot;
   volatile int* abort_v = abort_flag;
 
-  // producer lane: bit s of `armed` = ring slot s received a load, whose phase parity is bit s of armed_phase
+  // producer warp: bit s of `armed` = ring slot s received a load, whose phase parity is bit s of armed_phase
   uint32_t armed = 0, armed_phase = 0;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = cluster; ok && u < units; u += nclusters) {
-        const Unit t = unit_at(p, u);
-        const int m0 = t.m0 + 128 * static_cast<int>(rank);
-        // boxes of 64 rows of W: two for a full unit, one for a 128-wide one
-        const int n0 = t.n0 + (t.width / 2) * static_cast<int>(rank);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
-          if (leader)
-            mbar_arrive_expect_tx(&full[stage], 2 * kOperandBytes + static_cast<uint32_t>(t.width) * kBK);
-          const uint32_t bar = peer_addr(&full[stage], 0);
+    // The whole warp walks the schedule and one elected lane issues, as for the MMAs.
+    const uint32_t full_leader = peer_addr(full, 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = cluster; ok && u < units; u += nclusters) {
+      const Unit t = unit_at(p, u);
+      const int m0 = t.m0 + 128 * static_cast<int>(rank);
+      // boxes of 64 rows of W: two for a full unit, one for a 128-wide one
+      const int n0 = t.n0 + (t.width / 2) * static_cast<int>(rank);
+      const uint32_t bytes = 2 * kOperandBytes + static_cast<uint32_t>(t.width) * kBK;   // of both CTAs
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          const uint32_t bar = full_leader + 8 * stage;
           tma_load_2d_pair(sA + stage * kOperandBytes, &map_a, bar, kb * kBK, m0);
           tma_load_2d_pair(sW + stage * kOperandBytes, &map_w, bar, kb * kBK, n0);
           if (t.width == 256)
             tma_load_2d_pair(sW + stage * kOperandBytes + kOperandBytes / 2, &map_w, bar, kb * kBK, n0 + 64);
-          armed |= 1u << stage;
-          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
-      }
-      if (!ok) {
-        set_status(p.status, kDevTimeout);
-        *abort_v = 1;
+        __syncwarp();
+        armed |= 1u << stage;
+        armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
+    if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     // first CTA only: the whole warp walks the schedule, one elected lane issues
@@ -299,6 +318,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       int stage = 0, slot = 0, acc = 0;
       uint32_t phase = 0, sphase = 0, tphase = 0;   // sphase: of slot 0's round
       bool ok = true, issued = false;
+      bool ready = false;     // of the current stage, seen during the one before
       bool wrapped = false;   // groups before the third have no earlier user of their TMEM columns
       for (int u = cluster; ok && u < units; u += nclusters) {
         const uint32_t idesc = unit_at(p, u).width == 256 ? idesc_mxf8(256, 256) : idesc_mxf8(256, 128);
@@ -310,20 +330,25 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         for (int kb = 0; kb < p.num_kb; ++kb) {
           const uint32_t id = kb & 3;
           const uint32_t sfa = tmem_base + kScaleCol + (slot & (kScaleTmemSlots - 1)) * kScaleSlotCols, sfb = sfa + 4;
-          if (id == 0) {
-            // the scales are in shared memory, and the group two before, which used the same
-            // TMEM columns, is done (its slot's round is the last one where slot < 2)
-            const int before = (slot + kScaleSlots - kScaleTmemSlots) & (kScaleSlots - 1);
-            if (!mbar_wait_warp(&sfull[slot], sphase, abort_v, kWaitLimitNs) ||
-                !mbar_wait_warp(&speer[slot], sphase, abort_v, kWaitLimitNs) ||
-                ((wrapped || slot >= kScaleTmemSlots) &&
-                 !mbar_wait_warp(&sempty[before], sphase ^ (slot < kScaleTmemSlots ? 1u : 0u), abort_v,
-                                 kWaitLimitNs))) {
-              ok = false;
-              break;
+          if (id == 0 || !ready) {
+            // The operands have arrived; for the first block of four also: the scales are in shared
+            // memory, and the group two before, which used the same TMEM columns, is done (its
+            // slot's round is the last one where slot < 2). One lane waits for each.
+            uint64_t* bar = &full[stage];
+            uint32_t parity = phase;
+            if (id == 0 && lane == 1) {
+              bar = &sfull[slot];
+              parity = sphase;
             }
+            if (id == 0 && lane == 2 && (wrapped || slot >= kScaleTmemSlots)) {
+              bar = &sempty[(slot + kScaleSlots - kScaleTmemSlots) & (kScaleSlots - 1)];
+              parity = sphase ^ (slot < kScaleTmemSlots ? 1u : 0u);
+            }
+            if (!mbar_wait_warp(bar, parity, abort_v, kWaitLimitNs)) { ok = false; break; }
           }
-          if (!mbar_wait_warp(&full[stage], phase, abort_v, kWaitLimitNs)) { ok = false; break; }
+          // the next stage's barrier is looked at here, so that its answer is there when it is needed
+          const int next = stage + 1 == kStages ? 0 : stage + 1;
+          ready = mbar_peek(&full[next], phase ^ (next == 0 ? 1u : 0u));
           tc_fence_after();
           const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
           const uint64_t wdesc = wdesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
@@ -339,9 +364,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
               umma_mxf8_pair(d_tmem, adesc + static_cast<uint64_t>(2 * k), wdesc + static_cast<uint64_t>(2 * k),
                              idesc | idesc_scale_id(id), sfa, sfb, (kb | k) != 0 ? 1u : 0u);
             umma_commit_pair(&empty[stage], 0x3);
-            if (last) umma_commit_pair(&sempty[slot], 0x3);
+            if (last) umma_commit_pair(&sempty[slot], 0x1);
           }
-          __syncwarp();
+          ready = __all_sync(0xffffffffu, ready);
           issued = true;
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
           if (last && ++slot == kScaleSlots) { slot = 0; sphase ^= 1u; wrapped = true; }
@@ -357,63 +382,56 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         __syncwarp();
         mbar_wait_warp(drain, 0, nullptr, kWaitLimitNs);
       }
-    } else {
-      // An arrival at the other CTA's barrier that releases earlier writes takes about 1,400
-      // cycles; here it holds up nobody.
-      const uint32_t speer_leader = peer_addr(speer, 0);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- scales
+    // First CTA only: both CTAs' 128 rows of A, all the unit's rows of W for each. The words of the
+    // next four blocks are on their way while these are handed over.
+    if (leader) {
       int slot = 0;
       uint32_t sphase = 0;
       bool ok = true;
       const int groups = (p.num_kb + 3) / 4;
-      for (int u = cluster; ok && u < units; u += nclusters) {
-        for (int g = 0; g < groups; ++g) {
-          if (!mbar_wait_warp(&sfull[slot], sphase, abort_v, kWaitLimitNs)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_cluster(speer_leader + 8 * slot);
-          __syncwarp();
-          if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+      const uint32_t peer = peer_addr(sS, 1) + lane * 16;
+      auto load = [&](int u, int g, uint32_t (&w)[16]) {
+        const Unit t = unit_at(p, u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = scale_word(p.a_scales, p.k_pitch, t.m0 + 32 * c + lane, p.M, g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          w[8 + c] = c * 32 < t.width ? scale_word(p.w_scales, p.k_pitch, t.n0 + 32 * c + lane, p.N, g) : kUnitScale;
+      };
+      uint32_t w[16];
+      int u = cluster, g = 0;
+      if (u < units) load(u, g, w);
+      while (u < units) {
+        int nu = u, ng = g + 1;
+        if (ng == groups) { ng = 0; nu += nclusters; }
+        uint32_t next[16];
+        if (nu < units) load(nu, ng, next);
+        if (!mbar_wait_warp(&sempty[slot], sphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+        uint4* dst = reinterpret_cast<uint4*>(sS + slot * kScaleSlotBytes) + lane;
+        const uint32_t far = peer + slot * kScaleSlotBytes;
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        st_cluster_v4(far, make_uint4(w[4], w[5], w[6], w[7]));
+#pragma unroll
+        for (int c = 1; c < 3; ++c) {
+          const uint4 v = make_uint4(w[4 * c + 4], w[4 * c + 5], w[4 * c + 6], w[4 * c + 7]);
+          dst[c * 32] = v;
+          st_cluster_v4(far + c * 512, v);
         }
+        // tcgen05.cp reads them through the async proxy, in both CTAs
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[slot]);
+        if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = next[c];
+        u = nu;
+        g = ng;
       }
       if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
     }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------- scales
-    // Both CTAs: this CTA's 128 rows of A, all the unit's rows of W. The words of the next
-    // four blocks are on their way while these are handed over.
-    int slot = 0;
-    uint32_t sphase = 0;
-    bool ok = true;
-    const int groups = (p.num_kb + 3) / 4;
-    auto load = [&](int u, int g, uint32_t (&w)[12]) {
-      const Unit t = unit_at(p, u);
-      const int m0 = t.m0 + 128 * static_cast<int>(rank) + lane;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = scale_word(p.a_scales, p.k_pitch, m0 + 32 * c, p.M, g);
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        w[4 + c] = c * 32 < t.width ? scale_word(p.w_scales, p.k_pitch, t.n0 + 32 * c + lane, p.N, g) : kUnitScale;
-    };
-    uint32_t w[12];
-    int u = cluster, g = 0;
-    if (u < units) load(u, g, w);
-    while (u < units) {
-      int nu = u, ng = g + 1;
-      if (ng == groups) { ng = 0; nu += nclusters; }
-      uint32_t next[12];
-      if (nu < units) load(nu, ng, next);
-      if (!mbar_wait_warp(&sempty[slot], sphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
-      uint4* dst = reinterpret_cast<uint4*>(sS + slot * kScaleSlotBytes) + lane;
-#pragma unroll
-      for (int c = 0; c < 3; ++c) dst[c * 32] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-      fence_proxy_async_smem();   // tcgen05.cp reads them through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sfull[slot]);
-      if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
-#pragma unroll
-      for (int c = 0; c < 12; ++c) w[c] = next[c];
-      u = nu;
-      g = ng;
-    }
-    if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;                 // TMEM lanes this warp may read
