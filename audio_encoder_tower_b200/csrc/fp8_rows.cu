@@ -91,6 +91,7 @@ template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads)
 quantize_fp8_kernel(const T* __restrict__ x, int64_t ldx, int rows, int cols, int blocks, const Divider by_blocks,
                     uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  grid_dependency();
   const int sub = threadIdx.x & 7;
   Chunk<T> c[kUnroll] = {};
   uint32_t row[kUnroll];
@@ -203,6 +204,7 @@ template <typename T, int kDelta, int NV, int WPR>
 __global__ void __launch_bounds__(kThreads, 1)
 norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
   __shared__ float shared[kWarps];
+  grid_dependency();
   constexpr int kRagged = 2;
   constexpr int kStep = WPR * kFp8Block;     // columns from one of a warp's blocks to its next
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -332,9 +334,8 @@ norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
 template <typename T, int kDelta, int NV, int WPR>
 cudaError_t launch_norm(const void* x, void* x_out, const NormParams& p, cudaStream_t s) {
   constexpr int rpb = kWarps / WPR;
-  norm_fp8_kernel<T, kDelta, NV, WPR><<<(p.rows + rpb - 1) / rpb, kThreads, 0, s>>>(
-      reinterpret_cast<const T*>(x), reinterpret_cast<T*>(x_out), p);
-  return cudaGetLastError();
+  return launch_overlapped(norm_fp8_kernel<T, kDelta, NV, WPR>, (unsigned)(((int64_t)p.rows + rpb - 1) / rpb), kThreads, 0,
+                           1, s, reinterpret_cast<const T*>(x), reinterpret_cast<T*>(x_out), p);
 }
 
 // A warp per row up to 16 blocks of 128 columns, four from there on (the registers hold 16
@@ -365,13 +366,8 @@ cudaError_t launch_quantize_t(const void* x, int64_t ldx, int rows, int cols, ui
   if (grid * per >= 1ll << 31) return cudaErrorInvalidValue;   // Divider's range; the caller checks
   const T* p = reinterpret_cast<const T*>(x);
   const bool wide = reinterpret_cast<uintptr_t>(x) % 32 == 0 && ldx * sizeof(T) % 32 == 0;
-  if (wide)
-    quantize_fp8_kernel<T, true><<<(unsigned)grid, kThreads, 0, s>>>(p, ldx, rows, cols, blocks, Divider(blocks), q,
-                                                                    scales);
-  else
-    quantize_fp8_kernel<T, false><<<(unsigned)grid, kThreads, 0, s>>>(p, ldx, rows, cols, blocks, Divider(blocks), q,
-                                                                     scales);
-  return cudaGetLastError();
+  return launch_overlapped(wide ? quantize_fp8_kernel<T, true> : quantize_fp8_kernel<T, false>, (unsigned)grid, kThreads,
+                           0, 1, s, p, ldx, rows, cols, blocks, Divider(blocks), q, scales);
 }
 
 }  // namespace

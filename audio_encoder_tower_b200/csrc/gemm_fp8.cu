@@ -229,7 +229,7 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
 }
 
 template <int kEpi, bool kGelu>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ CUtensorMap map_c, const GemmFp8Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -277,6 +277,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   volatile int* abort_v = abort_flag;
+  grid_dependency();   // global memory from here on
 
   // producer warp: bit s of `armed` = ring slot s received a load, whose phase parity is bit s of armed_phase
   uint32_t armed = 0, armed_phase = 0;
@@ -542,8 +543,7 @@ cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cud
   p.tail = 2 * tail <= ncl ? tail : 0;
   const int units = p.num_tiles + p.tail;
   const int clusters = units < ncl ? units : ncl;
-  gemm_fp8_kernel<kEpi, kGelu><<<2 * clusters, kThreads, kSmemBytes, stream>>>(m.a, m.w, m.c, p);
-  return cudaGetLastError();
+  return launch_overlapped(gemm_fp8_kernel<kEpi, kGelu>, 2 * clusters, kThreads, kSmemBytes, 2, stream, m.a, m.w, m.c, p);
 }
 
 }  // namespace

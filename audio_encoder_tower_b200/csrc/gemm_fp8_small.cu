@@ -122,6 +122,7 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     tmem_base = *tmem_slot;
   }
   volatile int* abort_v = abort_flag;
+  grid_dependency();   // global memory from here on
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -332,19 +333,9 @@ cudaError_t launch_bt(const CUtensorMap& map_a, const CUtensorMap& map_w, int sp
                                     (int)Cfg<BT>::kSmem) == cudaSuccess;
       }))
     return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((p.N + 127) / 128) * ((p.M + BT - 1) / BT) * split), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<BT>::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)split;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_small_kernel<BT>, map_a, map_w, p, out, out_kind, split);
+  const unsigned grid = (unsigned)(((p.N + 127) / 128) * ((p.M + BT - 1) / BT) * split);
+  return launch_overlapped(gemm_fp8_small_kernel<BT>, grid, kThreads, Cfg<BT>::kSmem, split, stream, map_a, map_w, p, out,
+                           out_kind, split);
 }
 
 }  // namespace
