@@ -84,7 +84,7 @@ constexpr int kScaleSlots = 4, kScaleTmemSlots = 2;    // in shared memory, in T
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr size_t kSmemBytes = 1024 + kStages * (size_t)(2 * kOperandBytes) + kEpiWarps * 4096 /*staging*/ +
-                              kScaleSlots * kScaleSlotBytes + kEpiWarps * 512 /*bias*/ + 512;
+                              kScaleSlots * kScaleSlotBytes + kEpiWarps * 512 /*bias*/ + 2048 /*amax*/ + 512;
 
 // Work units: tiles of 256 x 256 in row-major order, the last `tail` of them as two
 // halves of 128 columns, so that a last wave under half full keeps more SMs busy. A last
@@ -122,6 +122,88 @@ __device__ __forceinline__ void bias_act(float (&t)[n], const float* bias) {
   }
 }
 
+// Where the two warps of a narrow unit meet that hold the halves of the same rows' block of 128
+// columns: each writes its amax and reads the other's after a barrier of the two. The buffer
+// alternates with the accumulator, so a warp may be one unit ahead of the other.
+struct Halves {
+  uint32_t* amax;   // [2][128] of this unit
+  int half, row, barrier;
+  __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory"); }
+  __device__ __forceinline__ uint32_t join(uint32_t v) const {
+    amax[half * 128 + row] = v;
+    sync();
+    return max(v, amax[(half ^ 1) * 128 + row]);
+  }
+};
+
+// e4m3 epilogue of 32 rows by one warp: a block of 128 columns from n0 (n = 128), or this warp's
+// half of it (n = 64; n0 is the block's first column in both, taddr and bias the half's).
+// The thread's part of the row stays in registers until the block's scale is known. (Half a block
+// in each of 16 warps on full units as well keeps up with the MMAs where this is the slower side,
+// but 24000 x 5120 x 1280 with GELU takes 156 us so against 147: the chip is at its power limit,
+// and that form does more work. On narrow units the halves occupy warps that would be idle.)
+template <int n, bool kGelu, typename Release>
+__device__ __forceinline__ void epilogue_e4m3(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0,
+                                              uint32_t taddr, uint8_t* stage, const float* bias, const Halves& halves,
+                                              int lane, Release&& release) {
+  float v[n];
+#pragma unroll
+  for (int c = 0; c < n; c += 32) tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+  if (lane == 0) bulk_wait_read0();
+  tmem_wait_ld();
+  release();
+  __syncwarp();   // the previous store has read the staging tile
+  bias_act<kGelu, true>(v, bias);
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < n; j += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], fabsf(v[j + 2 * k])), fabsf(v[j + 2 * k + 1]));
+  }
+  uint32_t bits = __float_as_uint(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));   // passes over NaN
+  if constexpr (n == 64) bits = halves.join(bits);
+  // an infinity in a row: the largest finite magnitude instead (both halves' warps see the same)
+  if (__any_sync(0xffffffffu, bits >= 0x7F800000u)) {
+    bits = 0;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      bits = max(bits, finite_abs_bits(v[j]));
+      v[j] = fmaf(v[j], 0.f, v[j]);       // and the infinity turns into NaN
+    }
+    if constexpr (n == 64) {
+      halves.sync();                      // both have read what the other wrote
+      bits = halves.join(bits);
+    }
+  }
+  const uint32_t byte = e8m0_of_amax(bits);
+  const float inv = e8m0_inverse(byte);
+  const int piece0 = n == 64 ? 4 * halves.half : 0;   // of the row's eight 16-byte pieces
+  uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
+#pragma unroll
+  for (int j = 0; j < n / 16; ++j) {
+    float t[16];
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) mul2(t[k], t[k + 1], v[16 * j + k], v[16 * j + k + 1], inv, inv);
+    row[(piece0 + j) ^ (lane & 7)] = make_uint4(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]),
+                                                e4m3x4(t[8], t[9], t[10], t[11]), e4m3x4(t[12], t[13], t[14], t[15]));
+  }
+  fence_proxy_async_smem();
+  if constexpr (n == 64) halves.sync();
+  else __syncwarp();
+  if (n == 64 && halves.half) return;
+  if (lane == 0) {
+    tma_store_2d(map_c, stage, n0, r0);
+    bulk_commit();
+  }
+  const int r = r0 + lane, g = n0 / kFp8Block;
+  if (r < p.M) {
+    uint8_t* s = p.out_scales + (int64_t)r * p.out_pitch + g;
+    *s = static_cast<uint8_t>(byte);
+    if (g + 1 == fp8_blocks(p.N))
+      for (int i = g + 1; i < p.out_pitch; ++i) *++s = 127;
+  }
+}
+
 // Epilogue of 32 rows x `cols` columns (from output column n0) by one warp. `bias`: the
 // warp's copy of those columns' bias in shared memory, zeros where there is none. `release`
 // is called once, as soon as the columns shared with the other accumulator have been read.
@@ -130,100 +212,46 @@ template <int kEpi, bool kGelu, typename Release>
 __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0, int cols,
                                          uint32_t taddr, bool down, uint8_t* stage, const float* bias, int lane,
                                          Release&& release) {
-  if constexpr (kEpi == ENC_FP8_OUT_FP8) {
-    // One block of 128 columns of a row per thread, held in registers: its scale needs all of
-    // them. (Half a block in each of 16 warps, the halves' amax joined in shared memory, keeps
-    // up with the MMAs where this is the slower side, but 24000 x 5120 x 1280 with GELU takes
-    // 156 us so against 147: the chip is at its power limit, and that form does more work.)
-    float v[128];
+  constexpr int kChunk = kEpi == ENC_FP8_OUT_BF16 ? 64 : 32;   // 128 bytes of a row
+  const int nc = cols / kChunk;
+#pragma unroll 1
+  for (int i = 0; i < nc; ++i) {
+    const int c = (down ? nc - 1 - i : i) * kChunk;
+    if (n0 + c >= p.N) continue;
+    float v[kChunk];
 #pragma unroll
-    for (int c = 0; c < 128; c += 32) tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
-    if (lane == 0) bulk_wait_read0();
+    for (int j = 0; j < kChunk; j += 32)
+      tmem_ld_32x32b_x32(taddr + c + j, *reinterpret_cast<uint32_t(*)[32]>(&v[j]));
+    if (lane == 0) bulk_wait_read0();   // the previous store has read the staging tile
     tmem_wait_ld();
-    release();
-    __syncwarp();   // the previous store has read the staging tile
-    bias_act<kGelu, true>(v, bias);
-    float top[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i == 0) release();
+    __syncwarp();
+    if constexpr (kEpi == ENC_FP8_OUT_BF16) {
+      bias_act<kGelu, false>(v, bias + c);
+    } else {
+      bias_act<false, false>(v, bias + c);
+      if constexpr (kGelu) {   // fp32 keeps what the fast form would lose
 #pragma unroll
-    for (int j = 0; j < 128; j += 8) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], fabsf(v[j + 2 * k])), fabsf(v[j + 2 * k + 1]));
-    }
-    uint32_t bits = __float_as_uint(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));   // passes over NaN
-    if (bits >= 0x7F800000u) {              // an infinity in the row: the largest finite magnitude instead
-      bits = 0;
-#pragma unroll
-      for (int j = 0; j < 128; ++j) {
-        bits = max(bits, finite_abs_bits(v[j]));
-        v[j] = fmaf(v[j], 0.f, v[j]);       // and the infinity turns into NaN
+        for (int k = 0; k < kChunk; ++k) v[k] = gelu_erf(v[k]);
       }
     }
-    const uint32_t byte = e8m0_of_amax(bits);
-    const float inv = e8m0_inverse(byte);
     uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float t[16];
-#pragma unroll
-      for (int k = 0; k < 16; k += 2) mul2(t[k], t[k + 1], v[16 * j + k], v[16 * j + k + 1], inv, inv);
-      row[j ^ (lane & 7)] = make_uint4(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]),
-                                       e4m3x4(t[8], t[9], t[10], t[11]), e4m3x4(t[12], t[13], t[14], t[15]));
+      const float* t = v + kChunk / 8 * j;
+      if constexpr (kEpi == ENC_FP8_OUT_BF16)
+        row[j ^ (lane & 7)] = make_uint4(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]), pack_bf16x2(t[4], t[5]),
+                                         pack_bf16x2(t[6], t[7]));
+      else
+        row[j ^ (lane & 7)] = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
+                                         __float_as_uint(t[3]));
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(map_c, stage, n0, r0);
+      if constexpr (kEpi == ENC_FP8_OUT_RESID) tma_reduce_add_2d(map_c, stage, n0 + c, r0);
+      else tma_store_2d(map_c, stage, n0 + c, r0);
       bulk_commit();
-    }
-    const int r = r0 + lane, g = n0 / kFp8Block;
-    if (r < p.M) {
-      uint8_t* s = p.out_scales + (int64_t)r * p.out_pitch + g;
-      *s = static_cast<uint8_t>(byte);
-      if (g + 1 == fp8_blocks(p.N))
-        for (int i = g + 1; i < p.out_pitch; ++i) *++s = 127;
-    }
-  } else {
-    constexpr int kChunk = kEpi == ENC_FP8_OUT_BF16 ? 64 : 32;   // 128 bytes of a row
-    const int nc = cols / kChunk;
-#pragma unroll 1
-    for (int i = 0; i < nc; ++i) {
-      const int c = (down ? nc - 1 - i : i) * kChunk;
-      if (n0 + c >= p.N) continue;
-      float v[kChunk];
-#pragma unroll
-      for (int j = 0; j < kChunk; j += 32)
-        tmem_ld_32x32b_x32(taddr + c + j, *reinterpret_cast<uint32_t(*)[32]>(&v[j]));
-      if (lane == 0) bulk_wait_read0();   // the previous store has read the staging tile
-      tmem_wait_ld();
-      if (i == 0) release();
-      __syncwarp();
-      if constexpr (kEpi == ENC_FP8_OUT_BF16) {
-        bias_act<kGelu, false>(v, bias + c);
-      } else {
-        bias_act<false, false>(v, bias + c);
-        if constexpr (kGelu) {   // fp32 keeps what the fast form would lose
-#pragma unroll
-          for (int k = 0; k < kChunk; ++k) v[k] = gelu_erf(v[k]);
-        }
-      }
-      uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float* t = v + kChunk / 8 * j;
-        if constexpr (kEpi == ENC_FP8_OUT_BF16)
-          row[j ^ (lane & 7)] = make_uint4(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]), pack_bf16x2(t[4], t[5]),
-                                           pack_bf16x2(t[6], t[7]));
-        else
-          row[j ^ (lane & 7)] = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
-                                           __float_as_uint(t[3]));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kEpi == ENC_FP8_OUT_RESID) tma_reduce_add_2d(map_c, stage, n0 + c, r0);
-        else tma_store_2d(map_c, stage, n0 + c, r0);
-        bulk_commit();
-      }
     }
   }
 }
@@ -239,7 +267,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   uint8_t* stage_c = sW + kStages * kOperandBytes;                            // 4 KB per epilogue warp
   uint8_t* sS = stage_c + kEpiWarps * 4096;                                   // scale slots
   float* sB = reinterpret_cast<float*>(sS + kScaleSlots * kScaleSlotBytes);   // bias, 128 columns per epilogue warp
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kEpiWarps * 128);         // used in the first CTA
+  uint32_t* sX = reinterpret_cast<uint32_t*>(sB + kEpiWarps * 128);           // amax of half blocks, [2][2][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sX + 512);                     // used in the first CTA
   uint64_t* empty = full + kStages;
   uint64_t* sfull = empty + kStages;        // [4] scales of both CTAs written; used in the first CTA
   uint64_t* sempty = sfull + kScaleSlots;   // [4] MMAs that read the slot are done; used in the first CTA
@@ -445,11 +474,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     for (int u = cluster; u < units; u += nclusters) {
       const Unit t = unit_at(p, u);
       const int r0 = t.m0 + 128 * static_cast<int>(rank) + quarter * 32;
-      // e4m3 output: a row's block of 128 columns is one thread's, so a narrow unit is the first half's alone
-      const int per = kEpi == ENC_FP8_OUT_FP8 ? 128 : t.width / 2;
-      const int c0 = half * per, n0 = t.n0 + c0;
+      const int per = t.width / 2, c0 = half * per, n0 = t.n0 + c0;
       float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);   // N is a multiple of 16
-      if (p.bias && n0 + 4 * lane < p.N) b4 = __ldg(reinterpret_cast<const float4*>(p.bias + n0) + lane);
+      if (p.bias && 4 * lane < per && n0 + 4 * lane < p.N) b4 = __ldg(reinterpret_cast<const float4*>(p.bias + n0) + lane);
       reinterpret_cast<float4*>(bias)[lane] = b4;    // the previous unit's reads ended with a __syncwarp
       if (!mbar_wait(&tfull[acc], tphase, abort_v, kWaitLimitNs)) {
         set_status(p.status, kDevTimeout);
@@ -469,10 +496,20 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       // the first accumulator's last 32 columns are the second one's first
       const bool shares = acc ? c0 == 0 : c0 + per == 256;
       if (!shares) release();
-      if (c0 < t.width && n0 < p.N && r0 < p.M) {
+      // of a narrow e4m3 unit both halves take part where its block of 128 columns has any
+      const int first = kEpi == ENC_FP8_OUT_FP8 ? n0 & ~127 : n0;
+      if (first < p.N && r0 < p.M) {
         const uint32_t taddr =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(c0);
-        epilogue<kEpi, kGelu>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, bias, lane, release);
+        if constexpr (kEpi == ENC_FP8_OUT_FP8) {
+          const Halves halves{sX + acc * 256, half, quarter * 32 + lane, 1 + quarter};
+          if (t.width == 256)
+            epilogue_e4m3<128, kGelu>(p, &map_c, r0, first, taddr, stage, bias, halves, lane, release);
+          else   // one staging tile for both halves
+            epilogue_e4m3<64, kGelu>(p, &map_c, r0, first, taddr, stage - half * (4 * 4096), bias, halves, lane, release);
+        } else {
+          epilogue<kEpi, kGelu>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, bias, lane, release);
+        }
       }
       release();
       acc ^= 1;
