@@ -557,6 +557,8 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
                 out = _torch.empty((M, N), dtype=tdt, device=a.device)
                 fresh = (out,)
             dst = out
+    if status is not None and (status.dtype != _torch.int32 or status.numel() < 1 or status.get_device() != dev):
+        raise ValueError(f"status must be an int32 tensor on device {dev}")
     if dst.dtype != tdt or dst.shape != (M, N) or not dst.is_contiguous() or dst.get_device() != dev:
         raise ValueError(f"the output must be a contiguous {tdt} [{M}, {N}] tensor on device {dev}")
     _fp8_call(_LIB.enc_linear_fp8, "enc_linear_fp8", dev, stream, fresh, a.data_ptr(), a_scales.data_ptr(),

@@ -93,6 +93,23 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int pitch, int 
   return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(s + (int64_t)row * pitch) + g) : kUnitScale;
 }
 
+// GELU for a bf16 result, on packed pairs: gelu_fast2 with the clamped magnitude as the tail's
+// factor too, so that an infinite sum gives infinity (or the tail's last value, 2.6e-10 below 0).
+__device__ __forceinline__ void gelu_bf16_2(float& x0, float& x1) {
+  using namespace gelu_tail;
+  const float a0 = fminf(fabsf(x0), kA), a1 = fminf(fabsf(x1), kA);
+  float g0, g1;
+  fma2(g0, g1, c7, c7, a0, a1, c6, c6);
+  fma2(g0, g1, g0, g1, a0, a1, c5, c5);
+  fma2(g0, g1, g0, g1, a0, a1, c4, c4);
+  fma2(g0, g1, g0, g1, a0, a1, c3, c3);
+  fma2(g0, g1, g0, g1, a0, a1, c2, c2);
+  fma2(g0, g1, g0, g1, a0, a1, c1, c1);
+  fma2(g0, g1, g0, g1, a0, a1, c0, c0);
+  x0 = fmaf(-a0, ex2(g0), x0 < 0.f ? 0.f : x0);   // not fmaxf: NaN stays NaN
+  x1 = fmaf(-a1, ex2(g1), x1 < 0.f ? 0.f : x1);
+}
+
 // GELU for an e4m3 result, on packed pairs: max(x, 0) - |x| 2^G(|x|) as gelu_fast2, with
 // G = log2 Phi(-a) from a minimax polynomial of degree 5 over [0, 5.5] (relative error of the
 // result there at most 2.5e-4, a 250th of half an e4m3 step). Beyond, the polynomial keeps
@@ -107,7 +124,7 @@ __device__ __forceinline__ void gelu_e4m3_2(float& x0, float& x1) {
   fma2(g0, g1, g0, g1, a0, a1, c2, c2);
   fma2(g0, g1, g0, g1, a0, a1, c1, c1);
   fma2(g0, g1, g0, g1, a0, a1, c0, c0);
-  x0 = fmaf(-a0, ex2(g0), fmaxf(x0, 0.f));
+  x0 = fmaf(-a0, ex2(g0), fmaxf(x0, 0.f));   // NaN stays NaN by its magnitude; an infinity becomes NaN
   x1 = fmaf(-a1, ex2(g1), fmaxf(x1, 0.f));
 }
 

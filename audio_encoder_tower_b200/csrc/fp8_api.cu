@@ -87,7 +87,8 @@ enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, co
   if (out_kind < ENC_FP8_OUT_BF16 || out_kind > ENC_FP8_OUT_RESID || M < 0 || N <= 0 || K <= 0)
     return ENC_ERR_INVALID_ARG;
   if (gelu && out_kind == ENC_FP8_OUT_RESID) return ENC_ERR_INVALID_ARG;
-  if (K % 16 || N % 16) return ENC_ERR_UNSUPPORTED;
+  // tiles reach past the last row and column by up to 255: their indexes stay in 32 bits
+  if (K % 16 || N % 16 || M > INT32_MAX - 512 || N > INT32_MAX - 512) return ENC_ERR_UNSUPPORTED;
   if (M == 0) return ENC_OK;
   if (!A || !a_scales || !W || !w_scales || !out || (out_kind == ENC_FP8_OUT_FP8 && !out_scales))
     return ENC_ERR_INVALID_ARG;

@@ -116,8 +116,8 @@ __device__ __forceinline__ void bias_act(float (&t)[n], const float* bias) {
       gelu_e4m3_2(t[k], t[k + 1]);
       gelu_e4m3_2(t[k + 2], t[k + 3]);
     } else if constexpr (kGelu) {
-      gelu_fast2(t[k], t[k + 1]);
-      gelu_fast2(t[k + 2], t[k + 3]);
+      gelu_bf16_2(t[k], t[k + 1]);
+      gelu_bf16_2(t[k + 2], t[k + 3]);
     }
   }
 }

@@ -276,8 +276,8 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         }
         y = make_float4(t[0], t[1], t[2], t[3]);
       } else {
-        gelu_fast2(y.x, y.y);
-        gelu_fast2(y.z, y.w);
+        gelu_bf16_2(y.x, y.y);
+        gelu_bf16_2(y.z, y.w);
       }
     }
     if (out_kind == ENC_FP8_OUT_FP8) {

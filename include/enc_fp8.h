@@ -7,6 +7,8 @@
  * asynchronous on `stream`, nothing traps; host-detectable errors return before
  * any launch. These calls allocate nothing and keep nothing: the caller owns
  * every buffer, and calls on different streams are independent of each other.
+ * They can be captured into a graph. A kernel's set-up may overlap the end of the
+ * kernel before it in the stream; it touches memory only after that one is done.
  * Every buffer is on the current device, which must be an sm_100.
  * A call with no rows is ENC_OK and launches nothing.
  *
@@ -58,7 +60,9 @@ typedef enum enc_norm_kind {
  * with block scales:
  *   x' = x + delta (rounded to x_dtype);  x_out = x';  (q, scales) = norm(x')
  * The norm is that of the stored stream, so one call gives what an addition and
- * a norm of its result give. Statistics and the norm itself are in fp32.
+ * a norm of its result give. Statistics and the norm itself are in fp32: the sum of
+ * squares must stay within fp32's range (|x'| up to 2e17 at any d). A NaN in a row
+ * makes that row NaN, and no other.
  *   x       [rows, d] of x_dtype, row stride ldx
  *   delta   [rows, d] of delta_dtype, row stride ldd, or NULL (x' = x)
  *   gamma   fp32 [d], 16-byte aligned;  beta  fp32 [d] or NULL (zeros)
@@ -89,12 +93,14 @@ typedef enum enc_fp8_out {
  *   bias          fp32 [N], 16-byte aligned, or NULL
  *   out           as out_kind says, 16-byte aligned, overlapping none of the others
  *   out_scales    ENC_FP8_OUT_FP8 only, [M, enc_fp8_scale_pitch(N)]
- *   K, N          multiples of 16; at least 16
+ *   K, N          multiples of 16; at least 16. M and N at most 2^31 - 513
  *   status        device int (may be NULL) set to ENC_ERR_TIMEOUT if a bounded
  *                 wait inside the kernel runs out
- * An output element depends on its row of A, its row of W and bias alone; the
- * same call gives the same bits every time (ENC_FP8_OUT_RESID as well: every
- * element is added to once).
+ * The order in which an element's products are summed depends on M, N and K alone:
+ * the same call gives the same bits every time (ENC_FP8_OUT_RESID as well: every
+ * element is added to once). NaN in a row of A or W (an element or a scale) makes that
+ * row or column of the output NaN; sums past fp32's range are not finite, and NaN in
+ * e4m3.
  */
 ENC_API enc_status enc_linear_fp8(const void *A, const void *a_scales, const void *W, const void *w_scales,
                                   const float *bias, void *out, void *out_scales, int32_t out_kind, int32_t M,

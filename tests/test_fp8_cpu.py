@@ -100,7 +100,8 @@ def test_norm_refusals(lib, change, want):
 
 @pytest.mark.parametrize("change,want", [
     (dict(M=0), OK), (dict(M=0, a=None, out=None), OK), (dict(M=-1), INVALID), (dict(N=0), INVALID),
-    (dict(K=0), INVALID), (dict(K=24), UNSUPPORTED), (dict(N=40), UNSUPPORTED), (dict(kind=4), INVALID),
+    (dict(K=0), INVALID), (dict(K=24), UNSUPPORTED), (dict(N=40), UNSUPPORTED),
+    (dict(M=2 ** 31 - 1), UNSUPPORTED), (dict(N=2 ** 31 - 16), UNSUPPORTED), (dict(kind=4), INVALID),
     (dict(kind=-1), INVALID), (dict(kind=3, gelu=1), INVALID), (dict(kind=2), INVALID), (dict(a=None), INVALID),
     (dict(sa=None), INVALID), (dict(w=None), INVALID), (dict(sw=None), INVALID), (dict(out=None), INVALID),
     (dict(a=A + 8), INVALID), (dict(w=A + 8), INVALID), (dict(out=A + 8), INVALID), (dict(bias=A + 8), INVALID),
@@ -149,6 +150,7 @@ def test_python_refusals():
         lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 32), out_scales=s),
         lambda: B.linear_fp8(q, s, w, sw, resid=torch.zeros(4, 32), gelu=True),
         lambda: B.linear_fp8(q, s, w, sw, resid=torch.zeros(4, 32).bfloat16()),
+        lambda: B.linear_fp8(q, s, w, sw, status=torch.zeros(1, dtype=torch.int64)),
     ]
     for i, call in enumerate(bad):
         with pytest.raises(ValueError):

@@ -300,6 +300,43 @@ def test_linear_nan_stays_in_its_row():
         assert np.array_equal(np.isnan(got8), nan)
 
 
+@pytest.mark.parametrize("M", [20, 300, 2500])
+def test_linear_overflow(M):
+    """Sums past fp32's range are not finite (an infinity, or NaN where products of both signs are past it:
+    each is 2^160 times a number near one here), NaN in e4m3, where the rest of the block keeps the scale
+    of its largest finite value. M takes the kernel for few rows, narrow units and full ones."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(24)
+    N, K = (1280, 256) if M == 2500 else (272, 256)
+    a, sa, av = _operand(rng, M, K, spread=0)
+    w, sw, wv = _operand(rng, N, K, spread=0)
+    rows, cols = [3, M - 1], [7, 100, 130, N - 1]
+    for r in rows:      # 2^80 * 2^80 overflows; either alone does not
+        sa.view(torch.uint8)[r, :2] += 80
+        av[r] *= 2.0 ** 80
+    for c in cols:
+        sw.view(torch.uint8)[c, :2] += 80
+        wv[c] *= 2.0 ** 80
+    y = av @ wv.T
+    big = np.abs(y) > 3.5e38
+    assert big.sum() == len(rows) * len(cols)
+    for gelu in (False, True):
+        for out in ("fp32", "bf16"):
+            got = linear_fp8(a, sa, w, sw, out_dtype=out, gelu=gelu).double().cpu().numpy()
+            ok = ~big
+            ref = F8.linear(av, wv, None, gelu)
+            assert np.all(np.isfinite(got[ok]))
+            if not gelu:   # GELU takes minus infinity to zero
+                assert not np.any(np.isfinite(got[big]))
+            slack = 1.13 * _acc_slack(av, wv, K) + 1e-4 * np.abs(ref) + 5e-11 * np.abs(y)
+            assert np.all(np.abs(got - ref)[ok] <= (slack + HALF[out] * (np.abs(ref) + slack))[ok])
+    q, s = linear_fp8(a, sa, w, sw, out_dtype="fp8")
+    got, e = _deq(q, s)
+    assert np.array_equal(np.isnan(got), big)
+    _check_norm(np.where(big, 0, got), e, np.where(big, 0, y), np.where(big, 0, _acc_slack(av, wv, K)))
+
+
 def test_linear_row_does_not_depend_on_its_neighbours():
     """The same row, alone and among others, within a tile and in another one, gives the same bits per kernel
     variant, and the same call twice gives the same bits."""
