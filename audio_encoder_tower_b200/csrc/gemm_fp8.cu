@@ -71,11 +71,14 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint4
 //   warps 4..  epilogue: warps of a TMEM lane quarter split the tile's columns
 // TMEM has 512 columns: two accumulators of 256 and the scales do not fit side by side.
 // The accumulators overlap instead, by 32 columns: 0..255 and 224..479, scales from
-// 480. A tile's MMAs may start once the epilogue has read the 32 shared columns of the
-// tile before, which it therefore reads first; the rest of its work still overlaps the
-// next tile's MMAs.
+// 480. The half of a tile that shares them with the tile before may start once the epilogue
+// has read them there, which it therefore does first. Until then the MMAs of the tile's other
+// half run, over the first kEarly blocks of K (as N = 128 each; from there on N = 256), so that
+// the tensor cores do not wait for the epilogue between tiles.
 constexpr int kEpiWarp0 = 4;
 constexpr int kStages = 5;
+// blocks; below kStages and 4 (one group of scales). fc1 of 16 clips: 0 blocks 140.5 us, 2 137.2, 3 137.6 to 140.2
+constexpr int kEarly = 2;
 constexpr uint32_t kOperandBytes = 128 * kBK;          // per stage: this CTA's 128 rows of A, and of W
 constexpr uint32_t kTmemCols = 512, kAcc1 = 224, kScaleCol = 480, kScaleSlotCols = 12;
 constexpr uint32_t kScaleSlotBytes = 3 * 512;          // A: 128 rows, W: 256 rows
@@ -142,16 +145,17 @@ struct Halves {
 // in each of 16 warps on full units as well keeps up with the MMAs where this is the slower side,
 // but 24000 x 5120 x 1280 with GELU takes 156 us so against 147: the chip is at its power limit,
 // and that form does more work. On narrow units the halves occupy warps that would be idle.)
-template <int n, bool kGelu, typename Release>
+template <int n, bool kGelu, typename Release, typename Done>
 __device__ __forceinline__ void epilogue_e4m3(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0,
                                               uint32_t taddr, uint8_t* stage, const float* bias, const Halves& halves,
-                                              int lane, Release&& release) {
+                                              int lane, Release&& release, Done&& done) {
   float v[n];
 #pragma unroll
   for (int c = 0; c < n; c += 32) tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
   if (lane == 0) bulk_wait_read0();
   tmem_wait_ld();
   release();
+  done();
   __syncwarp();   // the previous store has read the staging tile
   bias_act<kGelu, true>(v, bias);
   float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -206,12 +210,12 @@ __device__ __forceinline__ void epilogue_e4m3(const GemmFp8Params& p, const CUte
 
 // Epilogue of 32 rows x `cols` columns (from output column n0) by one warp. `bias`: the
 // warp's copy of those columns' bias in shared memory, zeros where there is none. `release`
-// is called once, as soon as the columns shared with the other accumulator have been read.
-// Chunks run upwards or, with `down`, downwards, so that those come first.
-template <int kEpi, bool kGelu, typename Release>
+// is called once, as soon as the columns shared with the other accumulator have been read, and
+// `done` when all have been. Chunks run upwards or, with `down`, downwards, so that those come first.
+template <int kEpi, bool kGelu, typename Release, typename Done>
 __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0, int cols,
                                          uint32_t taddr, bool down, uint8_t* stage, const float* bias, int lane,
-                                         Release&& release) {
+                                         Release&& release, Done&& done) {
   constexpr int kChunk = kEpi == ENC_FP8_OUT_BF16 ? 64 : 32;   // 128 bytes of a row
   const int nc = cols / kChunk;
 #pragma unroll 1
@@ -225,6 +229,7 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
     if (lane == 0) bulk_wait_read0();   // the previous store has read the staging tile
     tmem_wait_ld();
     if (i == 0) release();
+    if (i + 1 == nc) done();
     __syncwarp();
     if constexpr (kEpi == ENC_FP8_OUT_BF16) {
       bias_act<kGelu, false>(v, bias + c);
@@ -274,7 +279,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   uint64_t* sempty = sfull + kScaleSlots;   // [4] MMAs that read the slot are done; used in the first CTA
   uint64_t* tfull = sempty + kScaleSlots;   // [2] accumulator complete
   uint64_t* tempty = tfull + 2;             // shared columns read; used in the first CTA
-  uint64_t* drain = tempty + 1;
+  uint64_t* tdone = tempty + 1;             // [2] accumulator read; used in the first CTA
+  uint64_t* drain = tdone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -287,7 +293,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int s = 0; s < kScaleSlots; ++s) { mbar_init(&sfull[s], 1); mbar_init(&sempty[s], 1); }
-    for (int a = 0; a < 2; ++a) mbar_init(&tfull[a], 1);
+    for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tdone[a], 2 * kEpiWarps); }
     mbar_init(tempty, 2 * kEpiWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -320,8 +326,10 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     for (int u = cluster; ok && u < units; u += nclusters) {
       const Unit t = unit_at(p, u);
       const int m0 = t.m0 + 128 * static_cast<int>(rank);
-      // boxes of 64 rows of W: two for a full unit, one for a 128-wide one
-      const int n0 = t.n0 + (t.width / 2) * static_cast<int>(rank);
+      // boxes of 64 rows of W: two for a full unit, one for a 128-wide one. An MMA takes its first
+      // N / 2 columns' rows from the first CTA and the rest from the second, so the blocks that run as
+      // N = 128 have their boxes alternate between the CTAs.
+      const int early = t.width == 256 ? min(kEarly, p.num_kb) : p.num_kb;
       const uint32_t bytes = 2 * kOperandBytes + static_cast<uint32_t>(t.width) * kBK;   // of both CTAs
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
@@ -329,9 +337,11 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = full_leader + 8 * stage;
           tma_load_2d_pair(sA + stage * kOperandBytes, &map_a, bar, kb * kBK, m0);
+          const int n0 = t.n0 + (kb < early ? 64 : 128) * static_cast<int>(rank);
           tma_load_2d_pair(sW + stage * kOperandBytes, &map_w, bar, kb * kBK, n0);
           if (t.width == 256)
-            tma_load_2d_pair(sW + stage * kOperandBytes + kOperandBytes / 2, &map_w, bar, kb * kBK, n0 + 64);
+            tma_load_2d_pair(sW + stage * kOperandBytes + kOperandBytes / 2, &map_w, bar, kb * kBK,
+                             n0 + (kb < early ? 128 : 64));
         }
         __syncwarp();
         armed |= 1u << stage;
@@ -346,53 +356,97 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     if (leader) {
       const uint64_t adesc0 = smem_desc_sw128(smem_u32(sA)), wdesc0 = smem_desc_sw128(smem_u32(sW));
       int stage = 0, slot = 0, acc = 0;
-      uint32_t phase = 0, sphase = 0, tphase = 0;   // sphase: of slot 0's round
+      uint32_t phase = 0, sphase = 0, tphase = 0, dphase = 0;   // sphase: of slot 0's round
       bool ok = true, issued = false;
-      bool ready = false;     // of the current stage, seen during the one before
       bool wrapped = false;   // groups before the third have no earlier user of their TMEM columns
+      // The operands of `stage` have arrived; for the first block of four also: the scales are in
+      // shared memory, and the group two before, which used the same TMEM columns, is done (its
+      // slot's round is the last one where slot < 2). One lane waits for each.
+      auto wait_operands = [&](bool first) {
+        uint64_t* bar = &full[stage];
+        uint32_t parity = phase;
+        if (first && lane == 1) {
+          bar = &sfull[slot];
+          parity = sphase;
+        }
+        if (first && lane == 2 && (wrapped || slot >= kScaleTmemSlots)) {
+          bar = &sempty[(slot + kScaleSlots - kScaleTmemSlots) & (kScaleSlots - 1)];
+          parity = sphase ^ (slot < kScaleTmemSlots ? 1u : 0u);
+        }
+        return mbar_wait_warp(bar, parity, abort_v, kWaitLimitNs);
+      };
+      auto copy_scales = [&](uint32_t sfa) {
+        const uint64_t sdesc = smem_desc_scales(smem_u32(sS + slot * kScaleSlotBytes));
+#pragma unroll
+        for (int c = 0; c < 3; ++c) tmem_cp_scales_pair(sfa + 4 * c, sdesc + c * (512 >> 4));
+      };
+      auto mmas = [&](uint32_t d, uint64_t ad, uint64_t wd, uint32_t idesc, uint32_t sfa, uint32_t sfb, int kb) {
+#pragma unroll
+        for (int k = 0; k < kBK / 32; ++k)   // +32 bytes along K inside the swizzled row
+          umma_mxf8_pair(d, ad + static_cast<uint64_t>(2 * k), wd + static_cast<uint64_t>(2 * k),
+                         idesc | idesc_scale_id(kb & 3), sfa, sfb, (kb | k) != 0 ? 1u : 0u);
+      };
       for (int u = cluster; ok && u < units; u += nclusters) {
-        const uint32_t idesc = unit_at(p, u).width == 256 ? idesc_mxf8(256, 256) : idesc_mxf8(256, 128);
-        // the tile before: its columns shared with this one's accumulator have been read
+        const bool full_width = unit_at(p, u).width == 256;
+        const int early = full_width ? min(kEarly, p.num_kb) : 0;
+        // the tile two before, which used this accumulator, has been read
+        if (!mbar_wait_warp(&tdone[acc], dphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (acc ? kAcc1 : 0u);
+        uint32_t sfa = tmem_base + kScaleCol + (slot & (kScaleTmemSlots - 1)) * kScaleSlotCols;
+        // early blocks: the half without shared columns (the first one of the first accumulator)
+        const int stage0 = stage;
+        const uint32_t half0 = static_cast<uint32_t>(acc), half1 = 1u - half0;
+        constexpr uint32_t kHalfRows = kOperandBytes >> 5;   // 64 rows, in the descriptor's units
+        for (int kb = 0; kb < early; ++kb) {
+          if (!wait_operands(kb == 0)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            if (kb == 0) copy_scales(sfa);
+            mmas(d_tmem + 128 * half0, adesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4),
+                 wdesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4) + half0 * kHalfRows, idesc_mxf8(256, 128),
+                 sfa, sfa + 4 + 4 * half0, kb);
+          }
+          __syncwarp();
+          issued = true;
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        // the columns that the tile before shares with this one have been read
         if (!mbar_wait_warp(tempty, tphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
         tphase ^= 1u;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (acc ? kAcc1 : 0u);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          const uint32_t id = kb & 3;
-          const uint32_t sfa = tmem_base + kScaleCol + (slot & (kScaleTmemSlots - 1)) * kScaleSlotCols, sfb = sfa + 4;
-          if (id == 0 || !ready) {
-            // The operands have arrived; for the first block of four also: the scales are in shared
-            // memory, and the group two before, which used the same TMEM columns, is done (its
-            // slot's round is the last one where slot < 2). One lane waits for each.
-            uint64_t* bar = &full[stage];
-            uint32_t parity = phase;
-            if (id == 0 && lane == 1) {
-              bar = &sfull[slot];
-              parity = sphase;
+        if (early > 0) {   // their other half
+          const bool last = early == p.num_kb;
+          if (elect_one()) {
+            int st = stage0;
+            for (int e = 0; e < early; ++e) {
+              mmas(d_tmem + 128 * half1, adesc0 + static_cast<uint64_t>(st) * (kOperandBytes >> 4),
+                   wdesc0 + static_cast<uint64_t>(st) * (kOperandBytes >> 4) + half1 * kHalfRows, idesc_mxf8(256, 128),
+                   sfa, sfa + 4 + 4 * half1, e);
+              umma_commit_pair(&empty[st], 0x3);
+              if (++st == kStages) st = 0;
             }
-            if (id == 0 && lane == 2 && (wrapped || slot >= kScaleTmemSlots)) {
-              bar = &sempty[(slot + kScaleSlots - kScaleTmemSlots) & (kScaleSlots - 1)];
-              parity = sphase ^ (slot < kScaleTmemSlots ? 1u : 0u);
-            }
-            if (!mbar_wait_warp(bar, parity, abort_v, kWaitLimitNs)) { ok = false; break; }
+            if (last) umma_commit_pair(&sempty[slot], 0x1);
           }
+          __syncwarp();
+          if (last && ++slot == kScaleSlots) { slot = 0; sphase ^= 1u; wrapped = true; }
+        }
+        const uint32_t idesc = full_width ? idesc_mxf8(256, 256) : idesc_mxf8(256, 128);
+        bool ready = false;     // the stage's operands, seen during the block before
+        for (int kb = early; kb < p.num_kb; ++kb) {
+          const uint32_t id = kb & 3;
+          if ((id == 0 || !ready) && !wait_operands(id == 0)) { ok = false; break; }
           // the next stage's barrier is looked at here, so that its answer is there when it is needed
           const int next = stage + 1 == kStages ? 0 : stage + 1;
           ready = mbar_peek(&full[next], phase ^ (next == 0 ? 1u : 0u));
           tc_fence_after();
-          const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
-          const uint64_t wdesc = wdesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4);
+          sfa = tmem_base + kScaleCol + (slot & (kScaleTmemSlots - 1)) * kScaleSlotCols;
           const bool last = id == 3 || kb + 1 == p.num_kb;
           if (elect_one()) {
-            if (id == 0) {
-              const uint64_t sdesc = smem_desc_scales(smem_u32(sS + slot * kScaleSlotBytes));
-#pragma unroll
-              for (int c = 0; c < 3; ++c) tmem_cp_scales_pair(sfa + 4 * c, sdesc + c * (512 >> 4));
-            }
-#pragma unroll
-            for (int k = 0; k < kBK / 32; ++k)   // +32 bytes along K inside the swizzled row
-              umma_mxf8_pair(d_tmem, adesc + static_cast<uint64_t>(2 * k), wdesc + static_cast<uint64_t>(2 * k),
-                             idesc | idesc_scale_id(id), sfa, sfb, (kb | k) != 0 ? 1u : 0u);
+            if (id == 0) copy_scales(sfa);
+            mmas(d_tmem, adesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4),
+                 wdesc0 + static_cast<uint64_t>(stage) * (kOperandBytes >> 4), idesc, sfa, sfa + 4, kb);
             umma_commit_pair(&empty[stage], 0x3);
             if (last) umma_commit_pair(&sempty[slot], 0x1);
           }
@@ -405,6 +459,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
         __syncwarp();
         acc ^= 1;
+        if (acc == 0) dphase ^= 1u;
       }
       if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
       if (issued) {   // every MMA done before the pair's TMEM and shared memory go away
@@ -468,7 +523,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     const int half = (warp - kEpiWarp0) >> 2;     // which half of the unit's columns
     uint8_t* stage = stage_c + (warp - kEpiWarp0) * 4096;
     float* bias = sB + (warp - kEpiWarp0) * 128;
-    const uint32_t tempty_leader = peer_addr(tempty, 0);
+    const uint32_t tempty_leader = peer_addr(tempty, 0), tdone_leader = peer_addr(tdone, 0);
     int acc = 0;
     uint32_t tphase = 0;
     for (int u = cluster; u < units; u += nclusters) {
@@ -493,6 +548,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader);
       };
+      bool finished = false;
+      auto done = [&]() {
+        if (finished) return;
+        finished = true;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(tdone_leader + 8 * acc);
+      };
       // the first accumulator's last 32 columns are the second one's first
       const bool shares = acc ? c0 == 0 : c0 + per == 256;
       if (!shares) release();
@@ -504,14 +567,16 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         if constexpr (kEpi == ENC_FP8_OUT_FP8) {
           const Halves halves{sX + acc * 256, half, quarter * 32 + lane, 1 + quarter};
           if (t.width == 256)
-            epilogue_e4m3<128, kGelu>(p, &map_c, r0, first, taddr, stage, bias, halves, lane, release);
+            epilogue_e4m3<128, kGelu>(p, &map_c, r0, first, taddr, stage, bias, halves, lane, release, done);
           else   // one staging tile for both halves
-            epilogue_e4m3<64, kGelu>(p, &map_c, r0, first, taddr, stage - half * (4 * 4096), bias, halves, lane, release);
+            epilogue_e4m3<64, kGelu>(p, &map_c, r0, first, taddr, stage - half * (4 * 4096), bias, halves, lane,
+                                     release, done);
         } else {
-          epilogue<kEpi, kGelu>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, bias, lane, release);
+          epilogue<kEpi, kGelu>(p, &map_c, r0, n0, per, taddr, acc == 0, stage, bias, lane, release, done);
         }
       }
       release();
+      done();
       acc ^= 1;
       if (acc == 0) tphase ^= 1u;
     }
