@@ -110,6 +110,23 @@ __device__ __forceinline__ void gelu_bf16_2(float& x0, float& x1) {
   x1 = fmaf(-a1, ex2(g1), x1 < 0.f ? 0.f : x1);
 }
 
+// GELU for an fp32 result, on packed pairs: the same form with G of degree 10 from a minimax fit
+// over [0, 6]. With fp32's roundings it is within 1.7 * 2^-24 (|x| + |GELU|) of GELU there, and
+// ex2 adds 2^-22 of the tail's at most 0.17; beyond 6 both are within 6e-9 of max(x, 0). erff
+// takes three times the instructions (23456 x 2384 x 256: 91 us).
+__device__ __forceinline__ void gelu_fp32_2(float& x0, float& x1) {
+  constexpr float c[11] = {-0.9999997019767761f,     -1.1511183977127075f,    -0.45912185311317444f,
+                           -0.052702922374010086f,   0.007291511632502079f,   -0.00025596003979444504f,
+                           -0.00016587991558481008f, 4.562117828754708e-05f,  -5.9832109400304034e-06f,
+                           4.178519361630606e-07f,   -1.2412963101837704e-08f};
+  const float a0 = fminf(fabsf(x0), 16.f), a1 = fminf(fabsf(x1), 16.f);   // G keeps falling up to there
+  float g0 = c[10], g1 = c[10];
+#pragma unroll
+  for (int k = 9; k >= 0; --k) fma2(g0, g1, g0, g1, a0, a1, c[k], c[k]);
+  x0 = fmaf(-a0, ex2(g0), x0 < 0.f ? 0.f : x0);
+  x1 = fmaf(-a1, ex2(g1), x1 < 0.f ? 0.f : x1);
+}
+
 // GELU for an e4m3 result, on packed pairs: max(x, 0) - |x| 2^G(|x|) as gelu_fast2, with
 // G = log2 Phi(-a) from a minimax polynomial of degree 5 over [0, 5.5] (relative error of the
 // result there at most 2.5e-4, a 250th of half an e4m3 step). Beyond, the polynomial keeps

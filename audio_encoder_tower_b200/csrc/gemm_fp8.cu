@@ -235,9 +235,9 @@ __device__ __forceinline__ void epilogue(const GemmFp8Params& p, const CUtensorM
       bias_act<kGelu, false>(v, bias + c);
     } else {
       bias_act<false, false>(v, bias + c);
-      if constexpr (kGelu) {   // fp32 keeps what the fast form would lose
+      if constexpr (kGelu) {   // fp32 keeps what the shorter form would lose
 #pragma unroll
-        for (int k = 0; k < kChunk; ++k) v[k] = gelu_erf(v[k]);
+        for (int k = 0; k < kChunk; k += 2) gelu_fp32_2(v[k], v[k + 1]);
       }
     }
     uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);

@@ -267,14 +267,9 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     y = make_float4(y.x + bias.x, y.y + bias.y, y.z + bias.z, y.w + bias.w);
     const int64_t m = m0 + rank + ((int64_t)j << log), at = m * p.N + n;
     if (p.gelu) {
-      if (out_kind == ENC_FP8_OUT_FP32) {   // fp32 keeps what the fast form would lose
-        float t[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const float g = gelu_erf(t[0]);   // turned round once: each value in its place again
-          t[0] = t[1]; t[1] = t[2]; t[2] = t[3]; t[3] = g;
-        }
-        y = make_float4(t[0], t[1], t[2], t[3]);
+      if (out_kind == ENC_FP8_OUT_FP32) {   // fp32 keeps what the shorter form would lose
+        gelu_fp32_2(y.x, y.y);
+        gelu_fp32_2(y.z, y.w);
       } else {
         gelu_bf16_2(y.x, y.y);
         gelu_bf16_2(y.z, y.w);

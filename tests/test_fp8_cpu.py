@@ -119,7 +119,7 @@ def _mat(rows, cols):
 
 def test_python_refusals():
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
-    g = torch.ones(256)
+    g = torch.ones(256, dtype=torch.float32)
     q, s = _mat(4, 256)
     w, sw = _mat(32, 256)
     bad = [
@@ -145,10 +145,10 @@ def test_python_refusals():
         lambda: B.linear_fp8(q, s, w, sw, bias=g),
         lambda: B.linear_fp8(q, s, w, sw, out_dtype="fp16"),
         lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 32, dtype=torch.half)),
-        lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 16)),
-        lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 32), out_dtype="bf16"),
-        lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 32), out_scales=s),
-        lambda: B.linear_fp8(q, s, w, sw, resid=torch.zeros(4, 32), gelu=True),
+        lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 16, dtype=torch.float32)),
+        lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 32, dtype=torch.float32), out_dtype="bf16"),
+        lambda: B.linear_fp8(q, s, w, sw, out=torch.zeros(4, 32, dtype=torch.float32), out_scales=s),
+        lambda: B.linear_fp8(q, s, w, sw, resid=torch.zeros(4, 32, dtype=torch.float32), gelu=True),
         lambda: B.linear_fp8(q, s, w, sw, resid=torch.zeros(4, 32).bfloat16()),
         lambda: B.linear_fp8(q, s, w, sw, status=torch.zeros(1, dtype=torch.int64)),
     ]

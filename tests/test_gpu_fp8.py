@@ -358,7 +358,7 @@ def test_no_rows():
     from audio_encoder_tower_b200 import linear_fp8, norm_fp8, quantize_fp8
     x = torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda")
     q, s = quantize_fp8(x)
-    q2, s2, xo = norm_fp8(x, torch.ones(256, device="cuda"), delta=x)
+    q2, s2, xo = norm_fp8(x, torch.ones(256, dtype=torch.float32, device="cuda"), delta=x)
     w, sw, _ = _operand(np.random.default_rng(1), 32, 256)
     assert linear_fp8(q, s, w, sw).shape == (0, 32) and q2.shape == (0, 256) and xo.shape == (0, 256)
 
