@@ -421,37 +421,46 @@ def _fp8_call(fn, what, device, stream, fresh, *args):
         raise EncError(code, what)
 
 
-def _row_stride(t, device, what: str):
-    """(enc_dtype, row stride) of a bf16 or fp32 matrix whose rows are contiguous."""
+def _row_stride(t, shape, device, what: str):
+    """(enc_dtype, row stride) of a bf16 or fp32 matrix of that shape whose rows are contiguous."""
     dt = t.dtype
-    if (dt == _BF16 or dt == _FP32) and t.dim() == 2 and t.get_device() == device:
+    if (dt == _BF16 or dt == _FP32) and t.shape == shape and t.get_device() == device:
         code = ENC_DTYPE_BF16 if dt == _BF16 else ENC_DTYPE_FP32
         if t.is_contiguous():
-            return code, t.size(1)
-        if t.stride(1) == 1 or t.size(1) <= 1:
-            return code, (t.stride(0) if t.size(0) > 1 else t.size(1))
-    raise ValueError(f"{what} must be a bf16 or fp32 matrix with contiguous rows on device {device}")
+            return code, shape[1]
+        rs, cs = t.stride()
+        if cs == 1 or shape[1] <= 1:
+            return code, (rs if shape[0] > 1 else shape[1])
+    raise ValueError(f"{what} must be a bf16 or fp32 {list(shape)} matrix with contiguous rows on device {device}")
+
+
+def _matrix_shape(t, what: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be a matrix")
+    return shape
 
 
 def _check_fp8(q, scales, rows, cols, device, what: str):
     """An e4m3 [rows, cols] matrix with its block scales, both contiguous and on `device`."""
-    if q.dtype != _E4M3 or q.shape != (rows, cols) or not q.is_contiguous() or q.get_device() != device:
-        raise ValueError(f"{what} must be a contiguous float8_e4m3fn [{rows}, {cols}] tensor on device {device}")
-    if (scales.dtype != _E8M0 and scales.dtype != _U8) or not scales.is_contiguous() or \
-            scales.shape != (rows, (cols + 511) // 512 * 4) or scales.get_device() != device:
-        raise ValueError(f"the scales of {what} must be a contiguous float8_e8m0fnu "
-                         f"[{rows}, {fp8_scale_pitch(cols)}] tensor on device {device}")
+    st = scales.dtype
+    if q.dtype == _E4M3 and q.shape == (rows, cols) and q.get_device() == device and q.is_contiguous() and \
+            (st == _E8M0 or st == _U8) and scales.shape == (rows, (cols + 511) // 512 * 4) and \
+            scales.get_device() == device and scales.is_contiguous():
+        return
+    raise ValueError(f"{what} must be a contiguous float8_e4m3fn [{rows}, {cols}] tensor on device {device}, and its "
+                     f"scales a contiguous float8_e8m0fnu [{rows}, {fp8_scale_pitch(cols)}] tensor there")
 
 
 def _fp8_out(q, scales, rows, cols, like, what: str):
     """(q, scales, the tensors allocated here): the caller's output matrix, or a new one beside `like`."""
-    fresh = []
+    fresh = ()
     if q is None:
         q = _torch.empty((rows, cols), dtype=_E4M3, device=like.device)
-        fresh.append(q)
+        fresh += (q,)
     if scales is None:
         scales = _torch.empty((rows, fp8_scale_pitch(cols)), dtype=_E8M0, device=like.device)
-        fresh.append(scales)
+        fresh += (scales,)
     _check_fp8(q, scales, rows, cols, like.get_device(), what)
     return q, scales, fresh
 
@@ -473,8 +482,8 @@ def quantize_fp8(x, q=None, scales=None, stream=None):
     if _torch is None:
         _bind_torch()
     dev = x.get_device()
-    dtype, ldx = _row_stride(x, dev, "x")
-    rows, cols = x.shape
+    rows, cols = shape = _matrix_shape(x, "x")
+    dtype, ldx = _row_stride(x, shape, dev, "x")
     q, scales, fresh = _fp8_out(q, scales, rows, cols, x, "q")
     _fp8_call(_LIB.enc_quantize_fp8, "enc_quantize_fp8", dev, stream, fresh, x.data_ptr(), dtype, ldx, rows,
               cols, q.data_ptr(), scales.data_ptr())
@@ -494,23 +503,21 @@ def norm_fp8(x, gamma, beta=None, delta=None, kind="rms", eps=1e-5, x_out=None, 
     if gamma is None or (kind != "rms" and kind != "layer"):
         raise ValueError('gamma is required, and kind must be "rms" or "layer"')
     dev = x.get_device()
-    dtype, ldx = _row_stride(x, dev, "x")
-    rows, d = x.shape
+    rows, d = shape = _matrix_shape(x, "x")
+    dtype, ldx = _row_stride(x, shape, dev, "x")
     _check_vector(gamma, d, dev, "gamma")
     _check_vector(beta, d, dev, "beta")
     q, scales, fresh = _fp8_out(q, scales, rows, d, x, "q")
     ddtype, ldd, ldxo = ENC_DTYPE_BF16, d, d
     if delta is not None:
-        ddtype, ldd = _row_stride(delta, dev, "delta")
-        if delta.shape != x.shape:
-            raise ValueError("delta must have x's shape")
+        ddtype, ldd = _row_stride(delta, shape, dev, "delta")
         if x_out is None:
             x_out = _torch.empty((rows, d), dtype=x.dtype, device=x.device)
-            fresh.append(x_out)
+            fresh += (x_out,)
     if x_out is not None:
-        odtype, ldxo = _row_stride(x_out, dev, "x_out")
-        if odtype != dtype or x_out.shape != x.shape:
-            raise ValueError("x_out must have x's shape and type")
+        odtype, ldxo = _row_stride(x_out, shape, dev, "x_out")
+        if odtype != dtype:
+            raise ValueError("x_out must have x's type")
     _fp8_call(_LIB.enc_norm_fp8, "enc_norm_fp8", dev, stream, fresh,
               ENC_NORM_RMS if kind == "rms" else ENC_NORM_LAYER, x.data_ptr(), dtype, ldx,
               None if delta is None else delta.data_ptr(), ddtype, ldd, gamma.data_ptr(),
@@ -531,8 +538,8 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
     if _torch is None:
         _bind_torch()
     dev = a.get_device()
-    M, K = a.shape
-    N = w.size(0)
+    M, K = _matrix_shape(a, "a")
+    N = _matrix_shape(w, "w")[0]
     _check_fp8(a, a_scales, M, K, dev, "a")
     _check_fp8(w, w_scales, N, K, dev, "w")
     _check_vector(bias, N, dev, "bias")
@@ -543,27 +550,28 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
         kind, tdt, dst = ENC_FP8_OUT_RESID, _FP32, resid
     else:
         if out_dtype is None:
-            out_dtype = "bf16" if out is None or out.dtype == _BF16 else \
-                "fp32" if out.dtype == _FP32 else "fp8"
-        _expect(out_dtype in ("bf16", "fp32", "fp8"), 'the output type must be "bf16", "fp32" or "fp8"')
-        if out_dtype == "fp8":
-            out, out_scales, fresh = _fp8_out(out, out_scales, M, N, a, "out")
-            kind, tdt, dst = ENC_FP8_OUT_FP8, _E4M3, out
+            tdt = _BF16 if out is None else out.dtype
         else:
+            tdt = {"bf16": _BF16, "fp32": _FP32, "fp8": _E4M3}.get(out_dtype)
+        if tdt == _E4M3:
+            out, out_scales, fresh = _fp8_out(out, out_scales, M, N, a, "out")
+            kind = ENC_FP8_OUT_FP8
+        else:
+            kind = ENC_FP8_OUT_BF16 if tdt == _BF16 else ENC_FP8_OUT_FP32
+            _expect(kind == ENC_FP8_OUT_BF16 or tdt == _FP32, 'the output type must be "bf16", "fp32" or "fp8"')
             _expect(out_scales is None, "out_scales belong to an e4m3 output")
-            kind, tdt = (ENC_FP8_OUT_BF16, _BF16) if out_dtype == "bf16" else \
-                (ENC_FP8_OUT_FP32, _FP32)
             if out is None:
                 out = _torch.empty((M, N), dtype=tdt, device=a.device)
                 fresh = (out,)
-            dst = out
+        dst = out
     if status is not None and (status.dtype != _torch.int32 or status.numel() < 1 or status.get_device() != dev):
         raise ValueError(f"status must be an int32 tensor on device {dev}")
-    if dst.dtype != tdt or dst.shape != (M, N) or not dst.is_contiguous() or dst.get_device() != dev:
+    if dst.dtype != tdt or dst.shape != (M, N) or dst.get_device() != dev or not dst.is_contiguous():
         raise ValueError(f"the output must be a contiguous {tdt} [{M}, {N}] tensor on device {dev}")
     _fp8_call(_LIB.enc_linear_fp8, "enc_linear_fp8", dev, stream, fresh, a.data_ptr(), a_scales.data_ptr(),
               w.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(), dst.data_ptr(),
-              None if out_scales is None else out_scales.data_ptr(), kind, M, N, K, 1 if gelu else 0, _ptr(status))
+              None if out_scales is None else out_scales.data_ptr(), kind, M, N, K, 1 if gelu else 0,
+              None if status is None else status.data_ptr())
     return (out, out_scales) if kind == ENC_FP8_OUT_FP8 else dst
 
 
