@@ -88,7 +88,9 @@ enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, co
     return ENC_ERR_INVALID_ARG;
   if (gelu && out_kind == ENC_FP8_OUT_RESID) return ENC_ERR_INVALID_ARG;
   // tiles reach past the last row and column by up to 255: their indexes stay in 32 bits
-  if (K % 16 || N % 16 || M > INT32_MAX - 512 || N > INT32_MAX - 512) return ENC_ERR_UNSUPPORTED;
+  if (K % 16 || N % 16 || M > INT32_MAX - 512 || N > INT32_MAX - 512 ||
+      (int64_t)(M / 256 + 1) * (N / 256 + 1) > INT32_MAX / 2)
+    return ENC_ERR_UNSUPPORTED;
   if (M == 0) return ENC_OK;
   if (!A || !a_scales || !W || !w_scales || !out || (out_kind == ENC_FP8_OUT_FP8 && !out_scales))
     return ENC_ERR_INVALID_ARG;
@@ -100,7 +102,8 @@ enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, co
   const GemmFp8SmallPlan small = plan_gemm_fp8_small(M, N, K, sms);
   GemmFp8Maps m;
   if (!make_fp8_operand_map(&m.a, A, M, K, small.tile_m ? small.tile_m : 128) ||
-      !make_fp8_operand_map(&m.w, W, N, K, small.tile_m ? 128 : 64) || (!small.tile_m && !make_fp8_out_map(&m.c, out, out_kind, M, N)))
+      !make_fp8_operand_map(&m.w, W, N, K, small.tile_m ? 128 : 64) ||
+      (!small.tile_m && !make_fp8_out_map(&m.c, out, out_kind, M, N)))
     return ENC_ERR_CUDA;
   GemmFp8Params p;
   memset(&p, 0, sizeof(p));

@@ -63,7 +63,7 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint4
 
 // --------------------------------------------------------------- shape of the kernel
 // A cluster of two CTAs computes 256 x 256 tiles (M = 256 over the pair). CTA r holds
-// rows 128 r .. of the A tile and rows 128 r .. of the W tile in a ring of 32 KB stages.
+// rows 128 r .. of the A tile and half of the W tile's rows in a ring of 32 KB stages.
 //   warp 0   TMA producer;  warp 1  (first CTA) MMA issuer;  warp 3  none
 //   warp 2   (first CTA) scales of both CTAs, the second's by stores over the cluster: so one
 //            fence and one arrival in the issuer's own CTA cover them (an arrival from the other
@@ -75,10 +75,14 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint4
 // has read them there, which it therefore does first. Until then the MMAs of the tile's other
 // half run, over the first kEarly blocks of K (as N = 128 each; from there on N = 256), so that
 // the tensor cores do not wait for the epilogue between tiles.
+// Measured (one B200): 24000 x 5120 x 1280 with GELU to e4m3 137 to 141 us (2,290 TFLOP/s), 18737 x
+// 3840 x 1280 to bf16 82 us, 24000 x 1280 x 5120 122 us (2,580). Power bounds these: the SM clock is
+// 1.47 GHz with the tensor pipe busy 64% of the cycles at K = 1280 and 1.25 GHz with 86% at 5120.
+// Smaller grids are bound by an SM's intake from L2, about 58 bytes a cycle: 32 KB per 512 cycles of
+// MMAs for a full unit.
 constexpr int kEpiWarp0 = 4;
 constexpr int kStages = 5;
-// blocks; below kStages and 4 (one group of scales). fc1 of 16 clips: 0 blocks 140.5 us, 2 137.2, 3 137.6 to 140.2
-constexpr int kEarly = 2;
+constexpr int kEarly = 2;   // < kStages, < 4 (one group of scales). fc1: 0 blocks 140.5 us, 2 137.2, 3 138 to 140
 constexpr uint32_t kOperandBytes = 128 * kBK;          // per stage: this CTA's 128 rows of A, and of W
 constexpr uint32_t kTmemCols = 512, kAcc1 = 224, kScaleCol = 480, kScaleSlotCols = 12;
 constexpr uint32_t kScaleSlotBytes = 3 * 512;          // A: 128 rows, W: 256 rows
@@ -127,14 +131,15 @@ __device__ __forceinline__ void bias_act(float (&t)[n], const float* bias) {
 
 // Where the two warps of a narrow unit meet that hold the halves of the same rows' block of 128
 // columns: each writes its amax and reads the other's after a barrier of the two. The buffer
-// alternates with the accumulator, so a warp may be one unit ahead of the other.
+// alternates with the accumulator, so a warp may be one unit ahead of the other. (An mbarrier in
+// place of the hardware barrier makes the full unit's path spill: fc1 139 -> 156 us.)
 struct Halves {
   uint32_t* amax;   // [2][128] of this unit
   int half, row, barrier;
-  __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory"); }
+  __device__ __forceinline__ void meet() const { asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory"); }
   __device__ __forceinline__ uint32_t join(uint32_t v) const {
     amax[half * 128 + row] = v;
-    sync();
+    meet();
     return max(v, amax[(half ^ 1) * 128 + row]);
   }
 };
@@ -143,7 +148,7 @@ struct Halves {
 // half of it (n = 64; n0 is the block's first column in both, taddr and bias the half's).
 // The thread's part of the row stays in registers until the block's scale is known. (Half a block
 // in each of 16 warps on full units as well keeps up with the MMAs where this is the slower side,
-// but 24000 x 5120 x 1280 with GELU takes 156 us so against 147: the chip is at its power limit,
+// but 24000 x 5120 x 1280 with GELU took 156 us so against 147 then: the chip is at its power limit,
 // and that form does more work. On narrow units the halves occupy warps that would be idle.)
 template <int n, bool kGelu, typename Release, typename Done>
 __device__ __forceinline__ void epilogue_e4m3(const GemmFp8Params& p, const CUtensorMap* map_c, int r0, int n0,
@@ -175,7 +180,7 @@ __device__ __forceinline__ void epilogue_e4m3(const GemmFp8Params& p, const CUte
       v[j] = fmaf(v[j], 0.f, v[j]);       // and the infinity turns into NaN
     }
     if constexpr (n == 64) {
-      halves.sync();                      // both have read what the other wrote
+      halves.meet();                      // both have read what the other wrote
       bits = halves.join(bits);
     }
   }
@@ -192,7 +197,7 @@ __device__ __forceinline__ void epilogue_e4m3(const GemmFp8Params& p, const CUte
                                                 e4m3x4(t[8], t[9], t[10], t[11]), e4m3x4(t[12], t[13], t[14], t[15]));
   }
   fence_proxy_async_smem();
-  if constexpr (n == 64) halves.sync();
+  if constexpr (n == 64) halves.meet();
   else __syncwarp();
   if (n == 64 && halves.half) return;
   if (lane == 0) {
@@ -531,12 +536,16 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       const int r0 = t.m0 + 128 * static_cast<int>(rank) + quarter * 32;
       const int per = t.width / 2, c0 = half * per, n0 = t.n0 + c0;
       float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);   // N is a multiple of 16
-      if (p.bias && 4 * lane < per && n0 + 4 * lane < p.N) b4 = __ldg(reinterpret_cast<const float4*>(p.bias + n0) + lane);
+      if (p.bias && 4 * lane < per && n0 + 4 * lane < p.N)
+        b4 = __ldg(reinterpret_cast<const float4*>(p.bias + n0) + lane);
       reinterpret_cast<float4*>(bias)[lane] = b4;    // the previous unit's reads ended with a __syncwarp
       if (!mbar_wait(&tfull[acc], tphase, abort_v, kWaitLimitNs)) {
         set_status(p.status, kDevTimeout);
         *abort_v = 1;
-        break;
+        // The two warps of a narrow e4m3 unit meet at a barrier that nothing bounds: there a warp that
+        // gave up goes on (its output is void, and with the abort flag up its waits are short), so that
+        // the other one is not left waiting.
+        if constexpr (kEpi != ENC_FP8_OUT_FP8) break;
       }
       __syncwarp();
       tc_fence_after();
@@ -645,7 +654,8 @@ cudaError_t launch_pair(const GemmFp8Maps& m, GemmFp8Params p, int sm_count, cud
   p.tail = 2 * tail <= ncl ? tail : 0;
   const int units = p.num_tiles + p.tail;
   const int clusters = units < ncl ? units : ncl;
-  return launch_overlapped(gemm_fp8_kernel<kEpi, kGelu>, 2 * clusters, kThreads, kSmemBytes, 2, stream, m.a, m.w, m.c, p);
+  return launch_overlapped(gemm_fp8_kernel<kEpi, kGelu>, 2 * clusters, kThreads, kSmemBytes, 2, stream, m.a, m.w, m.c,
+                           p);
 }
 
 }  // namespace

@@ -59,8 +59,9 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 // Shared memory of this CTA to that of another of the cluster, counted on its barrier.
 __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :
+               : "r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
 
@@ -329,8 +330,8 @@ cudaError_t launch_bt(const CUtensorMap& map_a, const CUtensorMap& map_w, int sp
       }))
     return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(((p.N + 127) / 128) * ((p.M + BT - 1) / BT) * split);
-  return launch_overlapped(gemm_fp8_small_kernel<BT>, grid, kThreads, Cfg<BT>::kSmem, split, stream, map_a, map_w, p, out,
-                           out_kind, split);
+  return launch_overlapped(gemm_fp8_small_kernel<BT>, grid, kThreads, Cfg<BT>::kSmem, split, stream, map_a, map_w, p,
+                           out, out_kind, split);
 }
 
 }  // namespace

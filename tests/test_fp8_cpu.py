@@ -101,7 +101,8 @@ def test_norm_refusals(lib, change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(M=0), OK), (dict(M=0, a=None, out=None), OK), (dict(M=-1), INVALID), (dict(N=0), INVALID),
     (dict(K=0), INVALID), (dict(K=24), UNSUPPORTED), (dict(N=40), UNSUPPORTED),
-    (dict(M=2 ** 31 - 1), UNSUPPORTED), (dict(N=2 ** 31 - 16), UNSUPPORTED), (dict(kind=4), INVALID),
+    (dict(M=2 ** 31 - 1), UNSUPPORTED), (dict(M=2 ** 30, N=2 ** 20), UNSUPPORTED),
+    (dict(N=2 ** 31 - 16), UNSUPPORTED), (dict(kind=4), INVALID),
     (dict(kind=-1), INVALID), (dict(kind=3, gelu=1), INVALID), (dict(kind=2), INVALID), (dict(a=None), INVALID),
     (dict(sa=None), INVALID), (dict(w=None), INVALID), (dict(sw=None), INVALID), (dict(out=None), INVALID),
     (dict(a=A + 8), INVALID), (dict(w=A + 8), INVALID), (dict(out=A + 8), INVALID), (dict(bias=A + 8), INVALID),

@@ -26,7 +26,8 @@ def _rel(cfg, lengths, model, **kw):
 
 
 @pytest.mark.parametrize("cfg,lengths", [
-    (_small("std"), [333, 200, 1]), (_small("pp", pool_step=2, proj_hidden=256, proj_out=128, frames=120), [120, 51, 4]),
+    (_small("std"), [333, 200, 1]),
+    (_small("pp", pool_step=2, proj_hidden=256, proj_out=128, frames=120), [120, 51, 4]),
     (_small("ck", attn_chunk=7, frames=90), [90, 33, 2])], ids=["std", "pool_proj", "chunk"])
 def test_without_rounding_the_model_is_the_oracle(cfg, lengths):
     assert max(_rel(cfg, lengths, encode_clip_fp8, rounding=False)) < 1e-12
