@@ -197,7 +197,9 @@ def _acc_slack(a, w, K):
 
 SHAPES = [(1, 16, 16), (1, 128, 128), (1, 1280, 1280), (3, 272, 144), (16, 512, 1104), (50, 384, 1024), (64, 144, 640),
           (100, 1360, 512), (127, 256, 656), (128, 400, 128), (129, 128, 2064), (200, 1280, 1280), (257, 640, 1280),
-          (300, 272, 1168), (513, 1296, 272), (1000, 512, 528), (4000, 3840, 1280)]
+          (300, 272, 1168), (513, 1296, 272), (1000, 512, 528), (4000, 3840, 1280),
+          # few rows at a long depth; units of both widths in turn on one pair of SMs, several each
+          (33, 144, 2304), (90, 272, 4112), (400, 1280, 5120), (12000, 1360, 272), (7000, 1424, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
