@@ -384,19 +384,28 @@ def _expect(ok, what: str):
         raise ValueError(what)
 
 
-# What the 8-bit functions use of torch, looked up once: they cost a few microseconds of host
-# time per call, about as much as a small launch, so their common case takes the short way.
+# What the 8-bit functions use of torch, looked up once. A call through ctypes costs 8 to 12 us of
+# host time, more than a small launch takes on the device, so their usual case (outputs given, the
+# current stream, contiguous tensors) goes through the module _fastcall (csrc/fastcall.cpp) where
+# that has been built: 0 from it means launched, anything else takes the way below it.
 _torch = _BF16 = _FP32 = _E4M3 = _E8M0 = _U8 = _raw_stream = _cur_device = None
+_fast_quantize = _fast_norm = _fast_linear = None
 
 
 def _bind_torch():
     global _torch, _BF16, _FP32, _E4M3, _E8M0, _U8, _raw_stream, _cur_device
+    global _fast_quantize, _fast_norm, _fast_linear
     import torch
     _BF16, _FP32, _U8 = torch.bfloat16, torch.float32, torch.uint8
     _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
     _raw_stream, _cur_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _torch = torch
     load_library()
+    try:
+        from . import _fastcall
+        _fast_quantize, _fast_norm, _fast_linear = _fastcall.quantize, _fastcall.norm, _fastcall.linear
+    except ImportError:
+        _fast_quantize = _fast_norm = _fast_linear = lambda *args: -1
+    _torch = torch
 
 
 def _fp8_call(fn, what, device, stream, fresh, *args):
@@ -481,6 +490,8 @@ def quantize_fp8(x, q=None, scales=None, stream=None):
     """
     if _torch is None:
         _bind_torch()
+    if stream is None and q is not None and _fast_quantize(x, q, scales) == ENC_OK:
+        return q, scales
     dev = x.get_device()
     rows, cols = shape = _matrix_shape(x, "x")
     dtype, ldx = _row_stride(x, shape, dev, "x")
@@ -502,6 +513,10 @@ def norm_fp8(x, gamma, beta=None, delta=None, kind="rms", eps=1e-5, x_out=None, 
         _bind_torch()
     if gamma is None or (kind != "rms" and kind != "layer"):
         raise ValueError('gamma is required, and kind must be "rms" or "layer"')
+    number = ENC_NORM_RMS if kind == "rms" else ENC_NORM_LAYER
+    if stream is None and q is not None and (delta is None or x_out is not None) and \
+            _fast_norm(number, x, gamma, beta, delta, eps, x_out, q, scales) == ENC_OK:
+        return q, scales, x if x_out is None else x_out
     dev = x.get_device()
     rows, d = shape = _matrix_shape(x, "x")
     dtype, ldx = _row_stride(x, shape, dev, "x")
@@ -519,7 +534,7 @@ def norm_fp8(x, gamma, beta=None, delta=None, kind="rms", eps=1e-5, x_out=None, 
         if odtype != dtype:
             raise ValueError("x_out must have x's type")
     _fp8_call(_LIB.enc_norm_fp8, "enc_norm_fp8", dev, stream, fresh,
-              ENC_NORM_RMS if kind == "rms" else ENC_NORM_LAYER, x.data_ptr(), dtype, ldx,
+              number, x.data_ptr(), dtype, ldx,
               None if delta is None else delta.data_ptr(), ddtype, ldd, gamma.data_ptr(),
               None if beta is None else beta.data_ptr(), eps, rows, d, None if x_out is None else x_out.data_ptr(),
               ldxo, q.data_ptr(), scales.data_ptr())
@@ -537,6 +552,9 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
     """
     if _torch is None:
         _bind_torch()
+    if out is not None and stream is None and resid is None and out_dtype is None and status is None and \
+            _fast_linear(a, a_scales, w, w_scales, bias, out, out_scales, gelu) == ENC_OK:
+        return out if out_scales is None else (out, out_scales)
     dev = a.get_device()
     M, K = _matrix_shape(a, "a")
     N = _matrix_shape(w, "w")[0]

@@ -4,17 +4,21 @@
 
 Every .cu file under csrc/ is compiled for sm_100a (compute_100a) into
 _build/, then linked into audio_encoder_tower_b200/libenc_b200.so with the
-CUDA runtime linked statically.
+CUDA runtime linked statically. Where PyTorch is installed, csrc/fastcall.cpp is
+compiled as well (g++, no CUDA code): the short way from torch tensors to the
+8-bit operators' C calls. Without it the same calls go through ctypes.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +26,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libenc_b200.so")
+FASTCALL_SRC = os.path.join(CSRC, "fastcall.cpp")
+FASTCALL = os.path.join(HERE, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -51,8 +57,32 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_fastcall(force: bool = False) -> str | None:
+    """Compile csrc/fastcall.cpp against the installed PyTorch; None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    deps = [FASTCALL_SRC, os.path.join(INCLUDE, "enc_fp8.h"), os.path.join(INCLUDE, "enc.h")]
+    if not force and os.path.exists(FASTCALL) and all(os.path.getmtime(p) <= os.path.getmtime(FASTCALL) for p in deps):
+        return FASTCALL
+    torch = spec.submodule_search_locations[0]
+    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_path("include"), os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = FASTCALL + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *(x for d in inc for x in ("-isystem", d)), FASTCALL_SRC, "-o", tmp, "-L", HERE, "-lenc_b200",
+           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fastcall.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     if not force and up_to_date():
+        build_fastcall()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -78,6 +108,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_fastcall(force)
     return LIB
 
 

@@ -159,6 +159,27 @@ def test_python_refusals():
             pytest.fail(f"call {i} was not refused")
 
 
+def test_fastcall_leaves_anything_unusual_to_the_general_path():
+    """-1, without a call and without an exception, for wrong counts, types, devices and tensor subclasses."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    assert build.build_fastcall() is not None
+    B._bind_torch()
+    q, s = _mat(4, 256)
+    x, g = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.float32)
+    o = torch.zeros(4, 4, dtype=torch.bfloat16)
+    with FakeTensorMode():
+        fq = torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="cuda")
+        fs = torch.empty(4, 4, dtype=torch.float8_e8m0fnu, device="cuda")
+        fx, fo = torch.empty(4, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(4, 4, device="cuda")
+    calls = [(B._fast_quantize, a) for a in [(), (x,), (x, q, s), (None, q, s), (x, None, None), (1, 2, 3), (fx, fq, fs)]]
+    calls += [(B._fast_norm, a) for a in [(), (0, x, g, None, None, 1e-5, None, q, s), ("rms",) + (None,) * 8,
+                                          (0, fx, fx, None, None, 1e-5, None, fq, fs), (0,) * 9]]
+    calls += [(B._fast_linear, a) for a in [(), (q, s, q, s, None, o, None, False), (q, s, q, s, None, o, None, 1),
+                                            (fq, fs, fq, fs, None, fo, None, False), (None,) * 8]]
+    for f, a in calls:
+        assert f(*a) == -1
+
+
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
 def test_header_is_c99(tmp_path):
     src = tmp_path / "t.c"

@@ -355,6 +355,58 @@ def test_linear_row_does_not_depend_on_its_neighbours():
     assert torch.equal(part, full[perm])
 
 
+def test_both_ways_from_python():
+    """The short way (contiguous tensors, outputs given, the current stream) and the general one (the stream named)
+    make the same call, and a refusal is the same with outputs given."""
+    import torch
+    from audio_encoder_tower_b200 import EncError, binding, linear_fp8, norm_fp8, quantize_fp8
+    assert binding.fp8_scale_pitch(640) == 8
+    rng = np.random.default_rng(41)
+    x = _t(rng.standard_normal((70, 640)).astype(np.float32), torch.bfloat16)
+    g, b = _t(rng.standard_normal(640).astype(np.float32)), _t(rng.standard_normal(640).astype(np.float32))
+    w, sw, _ = _operand(rng, 272, 640)
+    bias = _t(rng.standard_normal(272).astype(np.float32))
+    cur = torch.cuda.current_stream()
+
+    def outs():
+        return (torch.empty(70, 640, dtype=torch.float8_e4m3fn, device="cuda"),
+                torch.empty(70, 8, dtype=torch.float8_e8m0fnu, device="cuda"))
+
+    def same(p, q):
+        assert all(torch.equal(a.view(torch.uint8), c.view(torch.uint8)) for a, c in zip(p, q))
+
+    q, s = quantize_fp8(x, *outs())
+    assert binding._fast_quantize(x, q, s) == 0
+    same((q, s), quantize_fp8(x, *outs(), stream=cur))
+    for kind, delta in (("rms", x), ("layer", x.float()), ("rms", None)):
+        xo = [torch.empty_like(x) if delta is not None else None for _ in range(2)]
+        q1, s1 = outs()
+        assert binding._fast_norm(0 if kind == "rms" else 1, x, g, b, delta, 1e-5, xo[0], q1, s1) == 0
+        first = norm_fp8(x, g, b, delta=delta, kind=kind, x_out=xo[0], q=q1, scales=s1)
+        q2, s2 = outs()
+        same(first, norm_fp8(x, g, b, delta=delta, kind=kind, x_out=xo[1], q=q2, scales=s2, stream=cur))
+    for T in (torch.bfloat16, torch.float32, torch.float8_e4m3fn):
+        o = [torch.empty(70, 272, dtype=T, device="cuda") for _ in range(2)]
+        so = [torch.empty(70, 4, dtype=torch.float8_e8m0fnu, device="cuda") if T == torch.float8_e4m3fn else None
+              for _ in range(2)]
+        assert binding._fast_linear(q, s, w, sw, bias, o[0], so[0], True) == 0
+        first = linear_fp8(q, s, w, sw, bias=bias, out=o[0], out_scales=so[0], gelu=True)
+        second = linear_fp8(q, s, w, sw, bias=bias, out=o[1], out_scales=so[1], gelu=True, stream=cur)
+        same(*((first, second) if isinstance(first, tuple) else ((first,), (second,))))
+    strided = x[:, :320]
+    q3, s3 = quantize_fp8(strided, q=torch.empty(70, 320, dtype=torch.float8_e4m3fn, device="cuda"),
+                          scales=torch.empty(70, 4, dtype=torch.float8_e8m0fnu, device="cuda"))
+    same((q3, s3), quantize_fp8(strided.contiguous()))
+    with pytest.raises(ValueError):
+        quantize_fp8(x, q=q[:69], scales=s)
+    with pytest.raises(ValueError):
+        linear_fp8(q, s, w, sw, out=torch.empty(70, 272, dtype=torch.float16, device="cuda"))
+    odd = torch.zeros(4, 24, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(EncError):
+        quantize_fp8(odd, q=torch.empty(4, 24, dtype=torch.float8_e4m3fn, device="cuda"),
+                     scales=torch.empty(4, 4, dtype=torch.float8_e8m0fnu, device="cuda"))
+
+
 def test_no_rows():
     import torch
     from audio_encoder_tower_b200 import linear_fp8, norm_fp8, quantize_fp8
