@@ -39,7 +39,11 @@ int sm_count_current() {
 }
 
 enc_status device_status(int sms) { return sms > 0 ? ENC_OK : sms < 0 ? ENC_ERR_UNSUPPORTED : ENC_ERR_CUDA; }
-enc_status launched(cudaError_t e) { return e == cudaSuccess ? ENC_OK : ENC_ERR_CUDA; }
+enc_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return ENC_OK;
+  cudaGetLastError();   // the error is the return value, not the next CUDA call's
+  return ENC_ERR_CUDA;
+}
 
 }  // namespace
 
