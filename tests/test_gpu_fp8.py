@@ -503,3 +503,36 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(out[i], alone[i])
+
+
+FIRST_CALL = """
+import torch
+from audio_encoder_tower_b200 import linear_fp8, norm_fp8, quantize_fp8
+g = torch.Generator("cuda").manual_seed(35)
+rand = lambda *s: torch.randn(*s, device="cuda", dtype=torch.float32, generator=g)
+wide, few, w, gamma = rand(700, 640), rand(5, 640), rand(384, 640), rand(640)
+def run():
+    wq = quantize_fp8(w)
+    return [t.view(torch.uint8) for x in (wide, few)
+            for q, s, _ in [norm_fp8(x, gamma, delta=x)]
+            for t in (q, s, linear_fp8(q, s, *wq, out_dtype="fp32"), *linear_fp8(q, s, *wq, out_dtype="fp8", gelu=True))]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = run()
+graph.replay()
+eager = run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, eager, strict=True))
+print("same")
+"""
+
+
+def test_first_call_of_a_process_is_captured():
+    """The one-time set-up of each kernel happens inside a capture as well."""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
