@@ -10,7 +10,9 @@
 // One tile per CTA, run once from start to end, so code size counts as well: an unrolled
 // epilogue spent most of its time fetching instructions. The loads start before the rest of
 // the set-up.
-//   warp 0  TMA producer;  warp 1  MMA issuer;  warp 2  scales;  then all four  epilogue
+//   warp 0  TMA producer;  warp 1  MMA issuer;  warp 2  scales;  then all of them  epilogue
+#include <math.h>
+
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -19,16 +21,19 @@ namespace enc {
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far above any legitimate wait
-constexpr int kThreads = 128;
 constexpr uint32_t kWBytes = 128 * kBK;
 constexpr int kScaleSlots = 4, kScaleTmemSlots = 2;                       // in shared memory, in TMEM
 constexpr uint32_t kScaleSlotBytes = 2 * 512;                             // 128 rows of W, up to 64 of A
 constexpr uint32_t kTmemCols = 256, kScaleCol = 128, kScaleSlotCols = 8;  // accumulator from column 0
 
 // Two CTAs per SM.
+// The epilogue takes a row per warp, one after another: the higher the tile, the more warps
+// (64 x 4192 x 192, tiles of 32 rows: 4.5 us with four warps, 3.9 with eight; 113 x 3568 x 1280,
+// of 64 rows: 6.9 with eight, 6.5 with sixteen). A call of up to 16 rows starts sooner with four.
 template <int BT>
 struct Cfg {
   static constexpr int kStages = BT == 16 ? 5 : BT == 64 ? 3 : 4;
+  static constexpr int kThreads = BT == 16 ? 128 : BT == 32 ? 256 : 512;
   static constexpr uint32_t kABytes = BT * kBK;
   static constexpr uint32_t kStageBytes = kWBytes + kABytes;
   static constexpr size_t kSmem = 1024 + kStages * (size_t)kStageBytes + BT * 512 /*partial sums*/ +
@@ -66,7 +71,7 @@ __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src,
 }
 
 template <int BT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Cfg<BT>::kThreads)
 gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                       const GemmFp8Params p, void* out, int out_kind, int split) {
   using C = Cfg<BT>;
@@ -114,11 +119,11 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
   if (split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   uint32_t tmem_base = 0;
   if (warp == 0) {
-    asm volatile("bar.arrive 1, 128;" ::: "memory");
+    asm volatile("bar.arrive 1, %0;" ::"n"(C::kThreads) : "memory");
   } else {
     if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
     tc_fence_before();
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory");
     tc_fence_after();
     tmem_base = *tmem_slot;
   }
@@ -225,13 +230,13 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
   // accumulators (lane = column of the output) to shared memory, by owner; rows past the tile's
   // last valid one go along up to the next multiple of 16
 #pragma unroll 1
-  for (int m = 0; m < rows; m += 16) {
+  for (int m = warp / 4 * 16; m < rows; m += C::kThreads / 8) {
     uint32_t v[16];
-    tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + m, v);
+    tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(warp % 4 * 32) << 16) + m, v);
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      outgoing[(((m + i) & (split - 1)) * per + ((m + i) >> log)) * 128 + threadIdx.x] = __uint_as_float(v[i]);
+      outgoing[(((m + i) & (split - 1)) * per + ((m + i) >> log)) * 128 + threadIdx.x % 128] = __uint_as_float(v[i]);
   }
   const float* sums = outgoing;
   if (split > 1) {
@@ -256,15 +261,19 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
   }
   const int stride = split > 1 ? mine * 128 : per * 128;   // from one rank's sums to the next
 #pragma unroll 1
-  for (int j = warp; j < mine; j += 4) {   // one row per warp
+  for (int j = warp; j < mine; j += C::kThreads / 32) {   // one row per warp
     const float4* s4 = reinterpret_cast<const float4*>(sums + j * 128) + lane;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (BT > 16 && split == 1) {
+      y = s4[0];
+    } else {
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      if (r < split) {
-        const float4 t = s4[r * stride / 4];
-        y = make_float4(y.x + t.x, y.y + t.y, y.z + t.z, y.w + t.w);
-      }
+      for (int r = 0; r < 8; ++r)
+        if (r < split) {
+          const float4 t = s4[r * stride / 4];
+          y = make_float4(y.x + t.x, y.y + t.y, y.z + t.z, y.w + t.w);
+        }
+    }
     y = make_float4(y.x + bias.x, y.y + bias.y, y.z + bias.z, y.w + bias.w);
     const int64_t m = m0 + rank + ((int64_t)j << log), at = m * p.N + n;
     if (p.gelu) {
@@ -330,29 +339,50 @@ cudaError_t launch_bt(const CUtensorMap& map_a, const CUtensorMap& map_w, int sp
       }))
     return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(((p.N + 127) / 128) * ((p.M + BT - 1) / BT) * split);
-  return launch_overlapped(gemm_fp8_small_kernel<BT>, grid, kThreads, Cfg<BT>::kSmem, split, stream, map_a, map_w, p,
+  return launch_overlapped(gemm_fp8_small_kernel<BT>, grid, Cfg<BT>::kThreads, Cfg<BT>::kSmem, split, stream, map_a, map_w, p,
                            out, out_kind, split);
 }
 
 }  // namespace
 
 GemmFp8SmallPlan plan_gemm_fp8_small(int M, int N, int K, int sm_count) {
-  // One tile per CTA, and no more CTAs than SMs (an eighth more where K is long and a CTA's
-  // work outweighs its start). Against the 256 x 256 kernel (us, this kernel first):
-  //   1 x 5120 x 1280  5.5 / 9.1    64 x 1280 x 1280   5.7 / 8.1    128 x 3840 x 1024  7.5 / 8.0
-  //   1 x 1280 x 5120  5.6 / 16.6   256 x 1280 x 1280  8.1 / 8.6    400 x 1280 x 5120  14.1 / 17.6
-  // and where it would lose: 128 x 5120 x 1280 9.6 / 8.7, 400 x 1280 x 1280 9.1 / 8.6,
-  // 700 x 1280 x 5120 18.5 / 18.0. Up to 32 rows it wins at any width (32 x 16384 x 1280
-  // 9.9 / 11.3): the other kernel would compute 256 rows.
+  // The time of this kernel and of the 256 x 256 one estimated (us), and the least taken. The
+  // coefficients are fitted to 700 shapes, M 1 to 3000, N 64 to 5200, K 100 to 6500: the choice
+  // is within 1% of the best one on the average. Per CTA: the blocks of K one after another, the
+  // tile's epilogue, with K split the exchange of the sums (both go with the tile's height), and
+  // what all the CTAs' loads cost each other. From about one CTA per SM on (somewhat fewer where
+  // clusters of 4 or 8 do not come out even in a GPC) some share an SM, which pays where each has
+  // a long way to go. Examples (this kernel / the other):
+  //   1 x 5120 x 1280  4.0 / 8.7    64 x 1280 x 1280   4.3 / 6.6    128 x 3840 x 1024  5.3 / 6.8
+  //   1 x 1280 x 5120  4.1 / 13.3   400 x 1280 x 1280  6.1 / 7.2    400 x 1280 x 5120  11.8 / 14.6
   const int kb = fp8_blocks(K);
-  const bool long_k = kb > 16;
-  const int bt = M <= 16 ? 16 : M <= 64 || !long_k ? 32 : 64;
-  const int64_t tiles = (int64_t)((N + 127) / 128) * ((M + bt - 1) / bt);
-  const int64_t limit = long_k ? sm_count * 9 / 8 : sm_count;
-  int split = 1;
-  while (split < 8 && 2 * split <= kb && tiles * 2 * split <= limit) split *= 2;
-  if (M > 32 && (tiles > limit || (long_k ? split < 2 : M > 256))) return {0, 0};
-  return {bt, split};
+  const int64_t columns = (N + 127) / 128, pair_tiles = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
+  GemmFp8SmallPlan plan = {0, 0};
+  float least;
+  if (M <= 32) {   // at any width, for the other kernel would compute 256 rows (32 x 16384 x 1280 7.7 / 10.5)
+    plan = {M <= 16 ? 16 : 32, 1};
+    least = INFINITY;
+  } else if (2 * pair_tiles <= sm_count) {   // a pair of SMs per tile or per half of one
+    const bool halves = 4 * pair_tiles <= sm_count;
+    least = 3.9f + 0.235f * kb + (halves ? 0.f : 2.45f) + 0.0029f * (halves ? 2 * pair_tiles : pair_tiles) * kb;
+  } else {
+    return plan;
+  }
+  for (int tile_m = 16; tile_m <= 64; tile_m *= 2)
+    for (int split = 1; split <= 8 && split <= kb; split *= 2) {
+      const int64_t ctas = columns * ((M + tile_m - 1) / tile_m) * split;
+      const int64_t over = ctas - sm_count + (split < 4 ? 0 : split == 4 ? 12 : 20);
+      if (ctas > 2 * sm_count) break;
+      const int depth = (kb + split - 1) / split;
+      const float t = 2.0f + 0.26f * depth + 0.012f * tile_m + (split > 1 ? 0.015f * tile_m : 0.f) +
+                      (split > 4 ? 0.2f : 0.f) + 2e-5f * ctas * depth * tile_m +
+                      (over > 0 ? 1.f + 0.2f * depth * over / sm_count : 0.f);
+      if (t < least) {
+        plan = {tile_m, split};
+        least = t;
+      }
+    }
+  return plan;
 }
 
 cudaError_t launch_gemm_fp8_small(const CUtensorMap& map_a, const CUtensorMap& map_w, const GemmFp8SmallPlan& plan,

@@ -199,7 +199,11 @@ SHAPES = [(1, 16, 16), (1, 128, 128), (1, 1280, 1280), (3, 272, 144), (16, 512, 
           (100, 1360, 512), (127, 256, 656), (128, 400, 128), (129, 128, 2064), (200, 1280, 1280), (257, 640, 1280),
           (300, 272, 1168), (513, 1296, 272), (1000, 512, 528), (4000, 3840, 1280),
           # few rows at a long depth; units of both widths in turn on one pair of SMs, several each
-          (33, 144, 2304), (90, 272, 4112), (400, 1280, 5120), (12000, 1360, 272), (7000, 1424, 144)]
+          (33, 144, 2304), (90, 272, 4112), (400, 1280, 5120), (12000, 1360, 272), (7000, 1424, 144),
+          # every height of tile with every split of K, then the 256 x 256 kernel on less than a wave of tiles
+          (628, 144, 144), (39, 176, 144), (82, 144, 480), (49, 144, 1296), (1373, 144, 176), (598, 144, 672),
+          (312, 144, 800), (81, 272, 2608), (1186, 432, 144), (1219, 144, 1680), (609, 144, 1840), (184, 576, 5168),
+          (1300, 1296, 2064), (2600, 400, 128), (1537, 1040, 4112), (257, 4240, 528), (2000, 4240, 16)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -251,7 +255,8 @@ def test_linear(M, N, K, out):
     assert int(status) == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 144, 640), (96, 272, 1168), (300, 512, 1280), (700, 1280, 528)])
+@pytest.mark.parametrize("M,N,K", [(5, 144, 640), (96, 272, 1168), (300, 512, 1280), (700, 1280, 528), (2000, 1280, 528),
+                                   (184, 576, 5168)])
 def test_linear_exact(M, N, K):
     """Small whole numbers under powers of two that differ from block to block: every partial sum
     is a number of fp32, so the result is the exact one in any order."""
@@ -272,7 +277,7 @@ def test_linear_scales_far_apart():
     """Block scales from 2^-60 to 2^60 on both sides, one block of each row far above the rest."""
     from audio_encoder_tower_b200 import linear_fp8
     rng = np.random.default_rng(21)
-    for M, N, K in ((40, 256, 1280), (400, 256, 1280)):
+    for M, N, K in ((40, 256, 1280), (400, 256, 1280), (2500, 1280, 640)):
         a, sa, av = _operand(rng, M, K, spread=30)
         w, sw, wv = _operand(rng, N, K, spread=30)
         got = linear_fp8(a, sa, w, sw, out_dtype="fp32").double().cpu().numpy()
@@ -284,7 +289,7 @@ def test_linear_nan_stays_in_its_row():
     import torch
     from audio_encoder_tower_b200 import linear_fp8
     rng = np.random.default_rng(22)
-    for M in (20, 300):
+    for M in (20, 300, 20000):
         a, sa, av = _operand(rng, M, 656)
         w, sw, wv = _operand(rng, 272, 656)
         a.view(torch.uint8)[3, 100] = 0x7F
