@@ -531,7 +531,7 @@ enc_status blocks_fp8(enc_handle* h, const Work& wk, const int* cu_att, cudaStre
   };
   auto norm = [&](const float* g, const float* b) {
     return launch_norm_fp8(ENC_NORM_LAYER, h->x, false, d, nullptr, false, d, g, b, c.ln_eps, R, d, nullptr, d,
-                           h->a8.q, h->a8.scales, s);
+                           h->a8.q, h->a8.scales, h->sm_count, s);
   };
   for (int l = 0; l < c.n_layers; ++l) {
     Range block("encoder block");

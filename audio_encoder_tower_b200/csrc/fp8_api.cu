@@ -82,7 +82,7 @@ enc_status enc_norm_fp8(int32_t kind, const void* x, int32_t x_dtype, int64_t ld
   if (sms <= 0) return device_status(sms);
   return launched(launch_norm_fp8(kind, x, x_dtype == ENC_DTYPE_BF16, ldx, delta, delta_dtype == ENC_DTYPE_BF16, ldd,
                                   gamma, beta, eps, rows, d, x_out, ldxo, reinterpret_cast<uint8_t*>(q),
-                                  reinterpret_cast<uint8_t*>(scales), stream));
+                                  reinterpret_cast<uint8_t*>(scales), sms, stream));
 }
 
 enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, const void* w_scales, const float* bias,

@@ -174,7 +174,6 @@ template <int WPR>
 __device__ __forceinline__ float row_sum(float v, float* shared, int warp) {
   v = warp_sum(v);
   if constexpr (WPR == 1) return v;
-  __syncthreads();   // the previous sum has been read
   if ((threadIdx.x & 31) == 0) shared[warp] = v;
   __syncthreads();
   const int w0 = warp / WPR * WPR;
@@ -190,22 +189,40 @@ struct NormParams {
   const void* delta;
   const float *gamma, *beta;
   float eps;
-  int rows, d;
+  int rows, d, sm_count;
   uint8_t *q, *scales;
 };
 
-// WPR warps per row, the row in registers: block i * WPR + part of 128 columns is the i-th of
-// warp `part`, four columns per lane. One read of each input and one write of each output:
-// memory bounds it (24000 x 1280 fp32 + bf16 53 us, 6.4 TB/s; 8191 x 4016 bf16 + bf16 40 us, 5.7).
-// Only the last kRagged of the NV blocks may lie past the
-// row's end. kDelta: 0 none, 1 bf16, 2 fp32.
 template <int kDelta> struct DeltaType { using type = bf16; };
 template <> struct DeltaType<2> { using type = float; };
 
+// Blocks per SM that the compiler's own choice of registers allows (126 for NV = 10, 198 for 16):
+// it keeps a row's loads together in front, and is the faster form where all rows run at once.
+constexpr int own_blocks(int nv) { return 512 / (12 * nv + 10); }
+// And with many rows: a row is a chain of latencies (loads, two sums over the warp, a block's maximum
+// before its scale), which other rows have to fill. Up to four bytes of input per column as many rows
+// as fit without spills, more still where the warps of a row wait for each other. Own choice against
+// this (us): 12000 x 1648 bf16 23.9 / 15.9, bf16 + bf16 31.2 / 22.8; 7118 x 4096 fp32 31.0 / 26.1;
+// 24000 x 1024 bf16 22.7 / 17.5; 8191 x 4016 bf16 + bf16 40.6 / 41.3; but 1500 x 1280 bf16 3.4 / 3.8.
 template <typename T, int kDelta, int NV, int WPR>
-__global__ void __launch_bounds__(kThreads, 1)   // without the 1 the loads are spread out: 58 us against 53.6
+constexpr int kManyBlocks = sizeof(T) + (kDelta == 0 ? 0 : kDelta == 1 ? 2 : 4) > 4 ? 512 / (6 * NV + 56)
+                            : NV > 12                                                  ? 512 / (4 * NV + 50)
+                            : WPR == 4                                                 ? 512 / (4 * NV + 38)
+                            : sizeof(T) == 2 && kDelta == 0                            ? 512 / (4 * NV + 32)
+                                                                                       : 512 / (4 * NV + 50);
+
+// WPR warps per row, the row in registers: block i * WPR + part of 128 columns is the i-th of
+// warp `part`, four columns per lane. One read of each input and one write of each output. With
+// six or eight bytes of input and output per column and more memory bounds it (24000 x 1280 fp32 +
+// bf16 53 us, 6.4 TB/s; 8191 x 4016 bf16 + bf16 41 us, 5.6), below that the row's latencies (24000 x
+// 1280 bf16 22.7 us, 4.1). Only the last kRagged of the NV blocks may lie past the row's end.
+// kDelta: 0 none, 1 bf16, 2 fp32.
+// kMany: for more rows than run at once with the compiler's choice. (The bound of one block is what
+// keeps the loads together: without it 24000 x 1280 fp32 + bf16 took 58 us against 53.6.)
+template <typename T, int kDelta, int NV, int WPR, bool kMany>
+__global__ void __launch_bounds__(kThreads, kMany ? kManyBlocks<T, kDelta, NV, WPR> : 1)
 norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
-  __shared__ float shared[kWarps];
+  __shared__ float shared[2][kWarps];   // of the two sums
   grid_dependency();
   constexpr int kRagged = 2;
   constexpr int kStep = WPR * kFp8Block;     // columns from one of a warp's blocks to its next
@@ -263,7 +280,7 @@ norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
       add2(s0, s1, s0, s1, v[i].x, v[i].y);
       add2(s0, s1, s0, s1, v[i].z, v[i].w);
     }
-    const float mean = row_sum<WPR>(s0 + s1, shared, warp) / d;
+    const float mean = row_sum<WPR>(s0 + s1, shared[0], warp) / d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const float m = inside(i) ? -mean : 0.f;   // columns past the end stay zero
@@ -277,7 +294,7 @@ norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
     fma2(s0, s1, v[i].x, v[i].y, v[i].x, v[i].y, s0, s1);
     fma2(s0, s1, v[i].z, v[i].w, v[i].z, v[i].w, s0, s1);
   }
-  const float rstd = 1.0f / sqrtf(row_sum<WPR>(s0 + s1, shared, warp) / d + p.eps);
+  const float rstd = 1.0f / sqrtf(row_sum<WPR>(s0 + s1, shared[1], warp) / d + p.eps);
   if (!live) return;
   uint8_t* qr = p.q + row * d + c0;
   const float* gr = p.gamma + c0;
@@ -337,7 +354,13 @@ template <typename T, int kDelta, int NV, int WPR>
 cudaError_t launch_norm(const void* x, void* x_out, const NormParams& p, cudaStream_t s) {
   constexpr int rpb = kWarps / WPR;
   const unsigned grid = (unsigned)(((int64_t)p.rows + rpb - 1) / rpb);
-  return launch_overlapped(norm_fp8_kernel<T, kDelta, NV, WPR>, grid, kThreads, 0, 1, s, reinterpret_cast<const T*>(x), reinterpret_cast<T*>(x_out), p);
+  if constexpr (kManyBlocks<T, kDelta, NV, WPR> > own_blocks(NV)) {
+    if (grid > (unsigned)(p.sm_count * own_blocks(NV)))
+      return launch_overlapped(norm_fp8_kernel<T, kDelta, NV, WPR, true>, grid, kThreads, 0, 1, s,
+                               reinterpret_cast<const T*>(x), reinterpret_cast<T*>(x_out), p);
+  }
+  return launch_overlapped(norm_fp8_kernel<T, kDelta, NV, WPR, false>, grid, kThreads, 0, 1, s,
+                           reinterpret_cast<const T*>(x), reinterpret_cast<T*>(x_out), p);
 }
 
 // A warp per row up to 16 blocks of 128 columns, four from there on (the registers hold 16
@@ -383,9 +406,9 @@ cudaError_t launch_quantize_fp8(const void* x, bool x_bf16, int64_t ldx, int row
 
 cudaError_t launch_norm_fp8(int kind, const void* x, bool x_bf16, int64_t ldx, const void* delta, bool delta_bf16,
                             int64_t ldd, const float* gamma, const float* beta, float eps, int rows, int d,
-                            void* x_out, int64_t ldxo, uint8_t* q, uint8_t* scales, cudaStream_t s) {
+                            void* x_out, int64_t ldxo, uint8_t* q, uint8_t* scales, int sm_count, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  const NormParams p{kind, ldx, ldd, ldxo, delta, gamma, beta, eps, rows, d, q, scales};
+  const NormParams p{kind, ldx, ldd, ldxo, delta, gamma, beta, eps, rows, d, sm_count, q, scales};
   return x_bf16 ? launch_norm_t<bf16>(x, x_out, p, delta_bf16, s) : launch_norm_t<float>(x, x_out, p, delta_bf16, s);
 }
 

@@ -136,7 +136,7 @@ cudaError_t launch_quantize_fp8(const void* x, bool x_bf16, int64_t ldx, int row
                                 uint8_t* scales, cudaStream_t s);
 cudaError_t launch_norm_fp8(int kind, const void* x, bool x_bf16, int64_t ldx, const void* delta, bool delta_bf16,
                             int64_t ldd, const float* gamma, const float* beta, float eps, int rows, int d,
-                            void* x_out, int64_t ldxo, uint8_t* q, uint8_t* scales, cudaStream_t s);
+                            void* x_out, int64_t ldxo, uint8_t* q, uint8_t* scales, int sm_count, cudaStream_t s);
 
 // --------------------------------------------------------- fp32 check path
 // C = A[M, K] (row stride lda, rows may overlap) * W[N, K]^T (row stride ldw).

@@ -145,6 +145,36 @@ def test_norm(rows, d, kind, x_type, delta_type):
     _check_norm(got, e, y, slack)
 
 
+@pytest.mark.parametrize("d", [16, 384, 512, 656, 1024, 1280, 1424, 1648, 2048, 2208, 4016, 5120, 5648, 7168, 8192])
+@pytest.mark.parametrize("x_type,delta_type", [("bf16", None), ("fp32", None), ("bf16", "bf16"), ("fp32", "fp32")])
+def test_norm_many_rows(d, x_type, delta_type):
+    """More rows than run at once take a kernel with other registers: the same bits, special rows among them,
+    in place, and rows behind the last one stay."""
+    import torch
+    from audio_encoder_tower_b200 import norm_fp8
+    rows = 14001 if d < 256 else 6001 if d <= 2048 else 1501
+    T = {"bf16": torch.bfloat16, "fp32": torch.float32}
+    g = torch.Generator("cuda").manual_seed(d)
+    rand = lambda *s: torch.randn(*s, device="cuda", dtype=torch.float32, generator=g)
+    x = rand(rows + 2, d).to(T[x_type])
+    delta = None if delta_type is None else rand(rows + 2, d).to(T[delta_type])
+    x[rows // 2], x[7, d - 1], x[rows - 1, 3] = 0, float("nan"), float("inf")
+    gamma, beta = rand(d), rand(d)
+    for kind in ("rms", "layer"):
+        y = x.clone()
+        q = torch.full((rows + 2, d), 0x55, dtype=torch.uint8, device="cuda")
+        s = torch.full((rows + 2, -(-d // 512) * 4), 0x55, dtype=torch.uint8, device="cuda")
+        norm_fp8(y[:rows], gamma, beta, delta=None if delta is None else delta[:rows], kind=kind, x_out=y[:rows],
+                 q=q[:rows].view(torch.float8_e4m3fn), scales=s[:rows])
+        assert bool((q[rows:] == 0x55).all()) and bool((s[rows:] == 0x55).all())
+        assert torch.equal(y[rows:], x[rows:])
+        for r in [*range(0, rows, 499)]:      # few enough to run at once
+            e = min(r + 499, rows)
+            a, b, o = norm_fp8(x[r:e], gamma, beta, delta=None if delta is None else delta[r:e], kind=kind)
+            assert torch.equal(a.view(torch.uint8), q[r:e]) and torch.equal(b.view(torch.uint8), s[r:e])
+            assert torch.equal(o.view(torch.uint8), y[r:e].view(torch.uint8))
+
+
 def test_norm_in_place_strides_and_neighbours():
     import torch
     from audio_encoder_tower_b200 import norm_fp8
