@@ -287,8 +287,25 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// The same, releasing at cluster scope: for a barrier whose waiter acts on another CTA's memory.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// kCluster: the wait acquires at cluster scope (otherwise at the CTA's).
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
+  if constexpr (kCluster) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  }
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -303,8 +320,19 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // sleeps in the instruction until the phase completes or about `hint_ns` have
 // passed, instead of returning at once to spin (a spinning warp takes issue
 // slots from the warps that share its scheduler).
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_test_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
   uint32_t ok;
+  if constexpr (kCluster) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(hint_ns)
+        : "memory");
+    return ok != 0;
+  }
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -319,13 +347,14 @@ __device__ __forceinline__ bool mbar_test_sleep(uint32_t bar, uint32_t parity, u
 // `limit_ns` nanoseconds or until *abort (when given) becomes non-zero. Returns false when
 // the wait gave up (the caller records the error and unwinds). Each retry sleeps for at
 // most 20 us, so the limit and the abort flag are looked at every 320 us or sooner.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
                                           uint64_t limit_ns) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_test(a, parity)) return true;
+  if (mbar_test<kCluster>(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_test_sleep(a, parity, 20000u)) return true;
+    if (mbar_test_sleep<kCluster>(a, parity, 20000u)) return true;
     if ((it & 15u) == 0u) {
       if (abort && *abort) return false;
       if (globaltimer_ns() - t0 > limit_ns) return false;

@@ -64,10 +64,15 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint4
 // --------------------------------------------------------------- shape of the kernel
 // A cluster of two CTAs computes 256 x 256 tiles (M = 256 over the pair). CTA r holds
 // rows 128 r .. of the A tile and half of the W tile's rows in a ring of 32 KB stages.
-//   warp 0   TMA producer;  warp 1  (first CTA) MMA issuer;  warp 3  none
-//   warp 2   (first CTA) scales of both CTAs, the second's by stores over the cluster: so one
-//            fence and one arrival in the issuer's own CTA cover them (an arrival from the other
-//            CTA that releases its writes took 1,500 cycles)
+//   warp 0   TMA producer;  warp 1  (first CTA) MMA issuer
+//   warps 2, 3  (first CTA) scales of both CTAs, the second's by stores over the cluster. The
+//            issuer's tcgen05.cp reads them in the other CTA's shared memory, so they are handed
+//            over at cluster scope: a proxy fence of every lane, an arrival that releases and a wait
+//            that acquires, on a barrier of the first CTA. Fence and release take about 900 and 1,200
+//            cycles, a group of four blocks 1,000 to 2,000: two warps in turn and four slots hide
+//            that but for a unit's first group. (A fence.acq_rel.cluster of every lane before the
+//            release: 24000 x 1280 x 5120 123 -> 134 us; instead of the release 124. An arrival
+//            from the second CTA would pay for the release as well.)
 //   warps 4..  epilogue: warps of a TMEM lane quarter split the tile's columns
 // TMEM has 512 columns: two accumulators of 256 and the scales do not fit side by side.
 // The accumulators overlap instead, by 32 columns: 0..255 and 224..479, scales from
@@ -378,7 +383,10 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
           bar = &sempty[(slot + kScaleSlots - kScaleTmemSlots) & (kScaleSlots - 1)];
           parity = sphase ^ (slot < kScaleTmemSlots ? 1u : 0u);
         }
-        return mbar_wait_warp(bar, parity, abort_v, kWaitLimitNs);
+        if (!first) return mbar_wait_warp(bar, parity, abort_v, kWaitLimitNs);
+        const bool seen = __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort_v, kWaitLimitNs));
+        __syncwarp();   // what lane 1 has acquired is the issuing lane's as well
+        return seen;
       };
       auto copy_scales = [&](uint32_t sfa) {
         const uint64_t sdesc = smem_desc_scales(smem_u32(sS + slot * kScaleSlotBytes));
@@ -473,32 +481,26 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         mbar_wait_warp(drain, 0, nullptr, kWaitLimitNs);
       }
     }
-  } else if (warp == 2) {
+  } else if (warp < kEpiWarp0) {
     // -------------------------------------------------------------- scales
-    // First CTA only: both CTAs' 128 rows of A, all the unit's rows of W for each. The words of the
-    // next four blocks are on their way while these are handed over.
+    // First CTA only: both CTAs' 128 rows of A, all the unit's rows of W for each. Two warps take
+    // turns with the groups of four blocks.
     if (leader) {
-      int slot = 0;
-      uint32_t sphase = 0;
       bool ok = true;
       const int groups = (p.num_kb + 3) / 4;
       const uint32_t peer = peer_addr(sS, 1) + lane * 16;
-      auto load = [&](int u, int g, uint32_t (&w)[16]) {
+      int u = cluster, g = warp - 2;
+      for (uint32_t i = warp - 2;; i += 2, g += 2) {   // the i-th group of this pair's schedule
+        while (g >= groups && u < units) { g -= groups; u += nclusters; }
+        if (u >= units) break;
         const Unit t = unit_at(p, u);
+        uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 8; ++c) w[c] = scale_word(p.a_scales, p.k_pitch, t.m0 + 32 * c + lane, p.M, g);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           w[8 + c] = c * 32 < t.width ? scale_word(p.w_scales, p.k_pitch, t.n0 + 32 * c + lane, p.N, g) : kUnitScale;
-      };
-      uint32_t w[16];
-      int u = cluster, g = 0;
-      if (u < units) load(u, g, w);
-      while (u < units) {
-        int nu = u, ng = g + 1;
-        if (ng == groups) { ng = 0; nu += nclusters; }
-        uint32_t next[16];
-        if (nu < units) load(nu, ng, next);
+        const uint32_t slot = i & (kScaleSlots - 1), sphase = (i / kScaleSlots) & 1u;
         if (!mbar_wait_warp(&sempty[slot], sphase ^ 1u, abort_v, kWaitLimitNs)) { ok = false; break; }
         uint4* dst = reinterpret_cast<uint4*>(sS + slot * kScaleSlotBytes) + lane;
         const uint32_t far = peer + slot * kScaleSlotBytes;
@@ -510,15 +512,11 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
           dst[c * 32] = v;
           st_cluster_v4(far + c * 512, v);
         }
-        // tcgen05.cp reads them through the async proxy, in both CTAs
+        // tcgen05.cp reads them through the async proxy, in both CTAs. The arrival releases every
+        // lane's stores (the warp has met) at cluster scope.
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[slot]);
-        if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) w[c] = next[c];
-        u = nu;
-        g = ng;
+        if (lane == 0) mbar_arrive_release_cluster(&sfull[slot]);
       }
       if (!ok && lane == 0) { set_status(p.status, kDevTimeout); *abort_v = 1; }
     }

@@ -571,3 +571,30 @@ def test_first_call_of_a_process_is_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 1280, 5120), (300, 272, 4112), (257, 4240, 1936), (12000, 768, 1040)])
+def test_linear_scales_reach_both_ctas(M, N, K):
+    """Scales that differ from block to block and from call to call, in calls queued one after another on pairs of
+    SMs: a group of scales that came late to the second SM of a pair would leave the one before in its place, off by
+    powers of two. All sums are whole numbers of 2^-6 below 2^24 of them, so every result is exact."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8, quantize_fp8
+    g = torch.Generator("cuda").manual_seed(M + N + K)
+    blocks = -(-K // 128)
+
+    def operand(rows):
+        v = torch.randint(-2, 3, (rows, K), generator=g, device="cuda").float()
+        e = torch.randint(-3, 4, (rows, blocks), generator=g, device="cuda").float()
+        x = v * torch.exp2(e).repeat_interleave(128, dim=1)[:, :K]
+        return (*quantize_fp8(x), x.double())
+
+    sets = [(operand(M), operand(N)) for _ in range(3)]
+    outs = [torch.empty(M, N, dtype=torch.float32, device="cuda") for _ in range(9)]
+    for i, o in enumerate(outs):
+        (a, sa, _), (w, sw, _) = sets[i % 3]
+        linear_fp8(a, sa, w, sw, out=o)
+    for i, o in enumerate(outs):
+        av, wv = sets[i % 3][0][2], sets[i % 3][1][2]
+        assert float((av.abs() @ wv.abs().t()).max()) * 64 < 2 ** 24
+        assert torch.equal(o.double(), av @ wv.t())
