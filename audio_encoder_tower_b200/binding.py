@@ -169,6 +169,21 @@ def _stream_handle(stream) -> int | None:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new_output(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one) to write. It comes from that
+    stream's memory, for a block that the current stream has freed may still have work queued there;
+    the current stream is recorded as a user, so that it may read the result until it is freed."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def encoder_config(*, n_mels, d_model, n_layers, n_heads, ffn_dim, max_frames, max_batch, dtype="bf16",
                    pool_step=1, proj_hidden=0, proj_out=0, ln_eps=1e-5, head_dim=64, attn_chunk=0,
                    guard=False, fp8=False) -> EncConfig:
@@ -408,24 +423,15 @@ def _bind_torch():
     _torch = torch
 
 
-def _fp8_call(fn, what, device, stream, fresh, *args):
+def _fp8_call(fn, what, device, stream, *args):
     """fn(*args, stream handle) on `device` (an ordinal, made current). stream=None is the
-    device's current stream; tensors allocated here (`fresh`) are marked as used on a stream
-    given by the caller."""
+    device's current stream."""
     if device < 0:
         raise ValueError("the tensors must be on a CUDA device")
     if device != _cur_device():
         with _torch.cuda.device(device):
-            return _fp8_call(fn, what, device, stream, fresh, *args)
-    if stream is None:
-        handle = _raw_stream(device)
-    else:
-        handle = _stream_handle(stream)
-        if fresh:
-            s = stream if isinstance(stream, _torch.cuda.Stream) else _torch.cuda.ExternalStream(handle)
-            for t in fresh:
-                t.record_stream(s)
-    code = fn(*args, handle)
+            return _fp8_call(fn, what, device, stream, *args)
+    code = fn(*args, _raw_stream(device) if stream is None else _stream_handle(stream))
     if code != ENC_OK:
         raise EncError(code, what)
 
@@ -461,17 +467,14 @@ def _check_fp8(q, scales, rows, cols, device, what: str):
                      f"scales a contiguous float8_e8m0fnu [{rows}, {fp8_scale_pitch(cols)}] tensor there")
 
 
-def _fp8_out(q, scales, rows, cols, like, what: str):
-    """(q, scales, the tensors allocated here): the caller's output matrix, or a new one beside `like`."""
-    fresh = ()
+def _fp8_out(q, scales, rows, cols, like, stream, what: str):
+    """(q, scales): the caller's output matrix, or a new one beside `like` for a call on `stream`."""
     if q is None:
-        q = _torch.empty((rows, cols), dtype=_E4M3, device=like.device)
-        fresh += (q,)
+        q = _new_output((rows, cols), _E4M3, like.device, stream)
     if scales is None:
-        scales = _torch.empty((rows, fp8_scale_pitch(cols)), dtype=_E8M0, device=like.device)
-        fresh += (scales,)
+        scales = _new_output((rows, fp8_scale_pitch(cols)), _E8M0, like.device, stream)
     _check_fp8(q, scales, rows, cols, like.get_device(), what)
-    return q, scales, fresh
+    return q, scales
 
 
 def _check_vector(v, n, device, what: str):
@@ -495,8 +498,8 @@ def quantize_fp8(x, q=None, scales=None, stream=None):
     dev = x.get_device()
     rows, cols = shape = _matrix_shape(x, "x")
     dtype, ldx = _row_stride(x, shape, dev, "x")
-    q, scales, fresh = _fp8_out(q, scales, rows, cols, x, "q")
-    _fp8_call(_LIB.enc_quantize_fp8, "enc_quantize_fp8", dev, stream, fresh, x.data_ptr(), dtype, ldx, rows,
+    q, scales = _fp8_out(q, scales, rows, cols, x, stream, "q")
+    _fp8_call(_LIB.enc_quantize_fp8, "enc_quantize_fp8", dev, stream, x.data_ptr(), dtype, ldx, rows,
               cols, q.data_ptr(), scales.data_ptr())
     return q, scales
 
@@ -522,18 +525,17 @@ def norm_fp8(x, gamma, beta=None, delta=None, kind="rms", eps=1e-5, x_out=None, 
     dtype, ldx = _row_stride(x, shape, dev, "x")
     _check_vector(gamma, d, dev, "gamma")
     _check_vector(beta, d, dev, "beta")
-    q, scales, fresh = _fp8_out(q, scales, rows, d, x, "q")
+    q, scales = _fp8_out(q, scales, rows, d, x, stream, "q")
     ddtype, ldd, ldxo = ENC_DTYPE_BF16, d, d
     if delta is not None:
         ddtype, ldd = _row_stride(delta, shape, dev, "delta")
         if x_out is None:
-            x_out = _torch.empty((rows, d), dtype=x.dtype, device=x.device)
-            fresh += (x_out,)
+            x_out = _new_output((rows, d), x.dtype, x.device, stream)
     if x_out is not None:
         odtype, ldxo = _row_stride(x_out, shape, dev, "x_out")
         if odtype != dtype:
             raise ValueError("x_out must have x's type")
-    _fp8_call(_LIB.enc_norm_fp8, "enc_norm_fp8", dev, stream, fresh,
+    _fp8_call(_LIB.enc_norm_fp8, "enc_norm_fp8", dev, stream,
               number, x.data_ptr(), dtype, ldx,
               None if delta is None else delta.data_ptr(), ddtype, ldd, gamma.data_ptr(),
               None if beta is None else beta.data_ptr(), eps, rows, d, None if x_out is None else x_out.data_ptr(),
@@ -561,7 +563,6 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
     _check_fp8(a, a_scales, M, K, dev, "a")
     _check_fp8(w, w_scales, N, K, dev, "w")
     _check_vector(bias, N, dev, "bias")
-    fresh = ()
     if resid is not None:
         _expect(out is None and out_dtype is None and out_scales is None and not gelu,
                 "resid takes no out, out_dtype, out_scales or gelu")
@@ -572,21 +573,20 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, out=None, out_dtype=None, ou
         else:
             tdt = {"bf16": _BF16, "fp32": _FP32, "fp8": _E4M3}.get(out_dtype)
         if tdt == _E4M3:
-            out, out_scales, fresh = _fp8_out(out, out_scales, M, N, a, "out")
+            out, out_scales = _fp8_out(out, out_scales, M, N, a, stream, "out")
             kind = ENC_FP8_OUT_FP8
         else:
             kind = ENC_FP8_OUT_BF16 if tdt == _BF16 else ENC_FP8_OUT_FP32
             _expect(kind == ENC_FP8_OUT_BF16 or tdt == _FP32, 'the output type must be "bf16", "fp32" or "fp8"')
             _expect(out_scales is None, "out_scales belong to an e4m3 output")
             if out is None:
-                out = _torch.empty((M, N), dtype=tdt, device=a.device)
-                fresh = (out,)
+                out = _new_output((M, N), tdt, a.device, stream)
         dst = out
     if status is not None and (status.dtype != _torch.int32 or status.numel() < 1 or status.get_device() != dev):
         raise ValueError(f"status must be an int32 tensor on device {dev}")
     if dst.dtype != tdt or dst.shape != (M, N) or dst.get_device() != dev or not dst.is_contiguous():
         raise ValueError(f"the output must be a contiguous {tdt} [{M}, {N}] tensor on device {dev}")
-    _fp8_call(_LIB.enc_linear_fp8, "enc_linear_fp8", dev, stream, fresh, a.data_ptr(), a_scales.data_ptr(),
+    _fp8_call(_LIB.enc_linear_fp8, "enc_linear_fp8", dev, stream, a.data_ptr(), a_scales.data_ptr(),
               w.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(), dst.data_ptr(),
               None if out_scales is None else out_scales.data_ptr(), kind, M, N, K, 1 if gelu else 0,
               None if status is None else status.data_ptr())

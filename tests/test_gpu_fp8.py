@@ -598,3 +598,40 @@ def test_linear_scales_reach_both_ctas(M, N, K):
         av, wv = sets[i % 3][0][2], sets[i % 3][1][2]
         assert float((av.abs() @ wv.abs().t()).max()) * 64 < 2 ** 24
         assert torch.equal(o.double(), av @ wv.t())
+
+
+def _queue_and_free(shape, dtype):
+    """Work on the current stream that starts late and writes and reads a tensor of that size, which is freed here:
+    the copy that was read."""
+    import torch
+    torch.cuda._sleep(20_000_000)      # 10 ms and more
+    return torch.full(shape, 1, dtype=torch.uint8 if dtype.itemsize == 1 else dtype, device="cuda").clone()
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_new_outputs_on_a_named_stream(as_handle):
+    """Outputs that a call on a named stream allocates are not memory in which the current stream still has work
+    queued: that work would overwrite them, or they its data."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8, norm_fp8, quantize_fp8
+    rng = np.random.default_rng(51)
+    M, K, N = 4096, 2048, 2560
+    x = _t(rng.standard_normal((M, K)).astype(np.float32), torch.bfloat16)
+    w, sw, _ = _operand(rng, N, K)
+    gamma = _t(np.ones(K, np.float32))
+    a, sa = quantize_fp8(x)
+    side = torch.cuda.Stream()
+    name = side.cuda_stream if as_handle else side
+    calls = [((M, K), torch.float8_e4m3fn, lambda s: quantize_fp8(x, stream=s)),
+             ((M, K), torch.bfloat16, lambda s: norm_fp8(x, gamma, delta=x, stream=s)),
+             ((M, N), torch.bfloat16, lambda s: (linear_fp8(a, sa, w, sw, stream=s),)),
+             ((M, N), torch.float32, lambda s: (linear_fp8(a, sa, w, sw, out_dtype="fp32", stream=s),)),
+             ((M, N), torch.float8_e4m3fn, lambda s: linear_fp8(a, sa, w, sw, out_dtype="fp8", stream=s))]
+    for shape, dtype, call in calls:
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        kept = _queue_and_free(shape, dtype)
+        got = call(name)
+        torch.cuda.synchronize()
+        assert bool((kept == 1).all())
+        assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(got, want, strict=True))
