@@ -277,11 +277,10 @@ class Encoder:
 
         Returns `out` [B, P_out, d_out] (allocated with torch when not given).
         """
-        import torch
         B = int(mel.shape[0])
         if out is None:
             _, p_out, d_out = self.output_positions(B, lengths)
-            out = torch.empty((B, p_out, d_out), dtype=mel.dtype, device=mel.device)
+            out = _new_output((B, p_out, d_out), mel.dtype, mel.device, stream)
         lp = None
         if lengths is not None:
             self._len = np.ascontiguousarray(lengths, dtype=np.int32)
@@ -297,11 +296,10 @@ class Encoder:
         `out` must be given by callers that cannot allocate; when omitted it is
         allocated here with torch for convenience.
         """
-        import torch
         B = int(mel.shape[0])
         if out is None:
             _, p_out, d_out = self.output_positions(B, lengths)
-            out = torch.empty((B, p_out, d_out), dtype=mel.dtype, device=mel.device)
+            out = _new_output((B, p_out, d_out), mel.dtype, mel.device, stream)
         lp = None
         if lengths is not None:
             self._len = np.ascontiguousarray(lengths, dtype=np.int32)
@@ -368,7 +366,7 @@ def linear_bf16(A, W, bias=None, out=None, resid=None, gelu=False, status=None, 
     M, K = A.shape
     N = W.shape[0]
     if out is None and resid is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _new_output((M, N), torch.bfloat16, A.device, stream)
     _check(load_library().enc_linear_bf16(_ptr(A), _ptr(W), _ptr(bias), _ptr(out), _ptr(resid), M, N, K,
                                           1 if gelu else 0, _ptr(status), _stream_handle(stream)),
            "enc_linear_bf16")
@@ -381,7 +379,7 @@ def attention_bf16(qkv, cu, max_n, n_heads, out=None, status=None, stream=None):
     R = qkv.shape[0]
     d = 64 * n_heads
     if out is None:
-        out = torch.empty((R, d), dtype=torch.bfloat16, device=qkv.device)
+        out = _new_output((R, d), torch.bfloat16, qkv.device, stream)
     _check(load_library().enc_attention_bf16(_ptr(qkv), _ptr(out), _ptr(cu), int(R), int(cu.numel()) - 1,
                                              int(max_n), int(n_heads), _ptr(status), _stream_handle(stream)),
            "enc_attention_bf16")
@@ -612,7 +610,7 @@ class Frontend:
             raise ValueError("audio must be a contiguous fp32 [B, 480000] device tensor")
         tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
         if out is None:
-            out = torch.empty((B, self.n_mels, self.FRAMES), dtype=tdt, device=audio.device)
+            out = _new_output((B, self.n_mels, self.FRAMES), tdt, audio.device, stream)
         _check(self.lib.enc_frontend_log_mel(self.h, _ptr(audio), int(B), _ptr(out), 0 if dtype == "bf16" else 1,
                                              _stream_handle(stream)), "enc_frontend_log_mel")
         return out
@@ -655,13 +653,12 @@ class Cache:
     def forward(self, mel, keys=None, lengths=None, out=None, stream=None):
         """Returns (out, hits): hits[b] = 1 where clip b's output came from the cache.
         keys=None derives each clip's key from its content (content_keys)."""
-        import torch
         B = int(mel.shape[0])
         if keys is None:
             keys = self.content_keys(mel, lengths, stream)
         if out is None:
             _, p_out, d_out = self.encoder.output_positions(B, lengths)
-            out = torch.empty((B, p_out, d_out), dtype=mel.dtype, device=mel.device)
+            out = _new_output((B, p_out, d_out), mel.dtype, mel.device, stream)
         k = np.ascontiguousarray(np.asarray(keys, dtype=np.uint64))
         if k.shape != (B,):
             raise ValueError("one key per clip")

@@ -142,3 +142,35 @@ def test_attention_bf16_many_short_segments():
         worst = max(worst, float(np.abs(got[s] - ref).max()))
         assert np.linalg.norm(got[s] - ref) / np.linalg.norm(ref) < 1e-2, b
     assert worst < 3e-2, worst
+
+
+def test_new_outputs_on_a_named_stream():
+    """Outputs that a call on a named stream allocates are not memory in which the current stream still has work
+    queued: that work would overwrite them, or they its data."""
+    import torch
+    from audio_encoder_tower_b200.binding import Frontend, attention_bf16, linear_bf16
+    from tests.encoder_cases import make_encoder, to_device
+    rng = np.random.default_rng(61)
+    a, w = _dev(rng.standard_normal((2000, 512)), torch.bfloat16), _dev(rng.standard_normal((640, 512)), torch.bfloat16)
+    qkv = _dev(rng.standard_normal((1500, 3 * 256)), torch.bfloat16)
+    cu = torch.tensor([0, 700, 1500], dtype=torch.int32, device="cuda")
+    cfg = S.EncoderConfig(name="stream", n_mels=80, d_model=256, n_layers=2, n_heads=4, ffn_dim=512, frames=300,
+                          batch=4, dtype="bf16", seed=22)
+    enc = make_encoder(cfg, to_device(cfg, S.make_weights(cfg)))
+    mel = torch.from_numpy(S.make_mel(cfg)).to(device="cuda", dtype=torch.bfloat16)
+    front = Frontend(n_mels=80, max_batch=2)
+    audio = _dev(0.1 * rng.standard_normal((2, Frontend.SAMPLES)), torch.float32)
+    side = torch.cuda.Stream()
+    for call in (lambda s: linear_bf16(a, w, stream=s), lambda s: attention_bf16(qkv, cu, 800, 4, stream=s),
+                 lambda s: enc.forward(mel, stream=s), lambda s: enc.forward_static_scratch(mel, stream=s),
+                 lambda s: front.log_mel(audio, stream=s)):
+        want = call(None)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)                  # 10 ms and more
+        kept = torch.ones_like(want).clone()           # the block that was read is freed here
+        got = call(side)
+        torch.cuda.synchronize()
+        assert bool((kept == 1).all()) and torch.equal(got, want)
+    enc.status()
+    front.close()
+    enc.close()
