@@ -276,14 +276,10 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     }
     y = make_float4(y.x + bias.x, y.y + bias.y, y.z + bias.z, y.w + bias.w);
     const int64_t m = m0 + rank + ((int64_t)j << log), at = m * p.N + n;
-    if (p.gelu) {
-      if (out_kind == ENC_FP8_OUT_FP32) {   // fp32 keeps what the shorter form would lose
-        gelu_fp32_2(y.x, y.y);
-        gelu_fp32_2(y.z, y.w);
-      } else {
-        gelu_bf16_2(y.x, y.y);
-        gelu_bf16_2(y.z, y.w);
-      }
+    const float4 sum = y;
+    if (p.gelu) {   // the form for fp32 whatever the output: rows are few
+      gelu_fp32_2(y.x, y.y);
+      gelu_fp32_2(y.z, y.w);
     }
     if (out_kind == ENC_FP8_OUT_FP8) {
       // the warp has a whole block of 128 columns (zeros past N)
@@ -291,10 +287,10 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
                          max(finite_abs_bits(y.z), finite_abs_bits(y.w)));
       const uint32_t byte = e8m0_of_amax(__reduce_max_sync(0xffffffffu, top));
       const float inv = e8m0_inverse(byte);
-      if (n < p.N)   // the products with zero turn an infinity into NaN
+      if (n < p.N)   // the products with zero turn an infinite sum into NaN, of which GELU may have made a zero
         *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(out) + at) =
-            e4m3x4(fmaf(y.x, 0.f, y.x * inv), fmaf(y.y, 0.f, y.y * inv), fmaf(y.z, 0.f, y.z * inv),
-                   fmaf(y.w, 0.f, y.w * inv));
+            e4m3x4(fmaf(sum.x, 0.f, y.x * inv), fmaf(sum.y, 0.f, y.y * inv), fmaf(sum.z, 0.f, y.z * inv),
+                   fmaf(sum.w, 0.f, y.w * inv));
       const int g = n0 / kFp8Block + lane;   // the block's scale, and after the row's last block the padding
       if (lane == 0 || (n0 + kFp8Block >= p.N && g < p.out_pitch))
         p.out_scales[m * p.out_pitch + g] = static_cast<uint8_t>(lane == 0 ? byte : 127u);

@@ -101,7 +101,12 @@ typedef enum enc_fp8_out {
  * the same call gives the same bits every time (ENC_FP8_OUT_RESID as well: every
  * element is added to once). NaN in a row of A or W (an element or a scale) makes that
  * row or column of the output NaN; sums past fp32's range are not finite, and NaN in
- * e4m3.
+ * e4m3, with GELU too. (In bf16 and fp32 GELU takes a sum of minus infinity to its limit,
+ * zero.)
+ *   GELU is x Phi(x) from a polynomial in |x| and one exponential, before the rounding to
+ * the output's type: with fp32 output within 2^-22 (|x| + |GELU|), with bf16 output within 1.1e-5
+ * of its value and 2.7e-10, with e4m3 output within 2.5e-4 of its value where |x| <= 5.5 and
+ * within 1.9e-8 |x| beyond.
  */
 ENC_API enc_status enc_linear_fp8(const void *A, const void *a_scales, const void *W, const void *w_scales,
                                   const float *bias, void *out, void *out_scales, int32_t out_kind, int32_t M,

@@ -635,3 +635,58 @@ def test_new_outputs_on_a_named_stream(as_handle):
         torch.cuda.synchronize()
         assert bool((kept == 1).all())
         assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(got, want, strict=True))
+
+
+@pytest.mark.parametrize("M", [1, 20, 300, 2500])
+def test_linear_overflow_with_gelu_in_e4m3(M):
+    """With GELU as without it, a sum past fp32's range is NaN in e4m3, whatever its sign and whichever kernel M
+    takes (few rows, narrow units, full ones), and the rest of its block keeps the scale of its finite values."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(52)
+    N, K = (1280, 256) if M == 2500 else (272, 256)
+    a, sa, av = _operand(rng, M, K, spread=0)
+    w, sw, wv = _operand(rng, N, K, spread=0)
+    row, cols = M - 1, [3, 7, 100, 130, 131, 133, N - 1]
+    sa.view(torch.uint8)[row, :2] += 80     # 2^80 * 2^80 overflows; either alone does not
+    av[row] *= 2.0 ** 80
+    for c in cols:
+        sw.view(torch.uint8)[c, :2] += 80
+        wv[c] *= 2.0 ** 80
+    wv[cols[::2]] *= -1
+    w.view(torch.uint8)[cols[::2]] ^= 0x80
+    y = av @ wv.T
+    big = np.abs(y) > 3.5e38
+    assert big.sum() == len(cols) and (y[big] > 0).any() and (y[big] < 0).any()
+    q, s = linear_fp8(a, sa, w, sw, out_dtype="fp8", gelu=True)
+    got, e = _deq(q, s)
+    assert np.array_equal(np.isnan(got), big)
+    y = np.where(big, 0, y)
+    ref = F8.gelu(y)
+    slack = 1.13 * _acc_slack(av, wv, K) + 2.6e-4 * np.abs(ref) + 2e-8 * np.abs(y)      # as in test_linear
+    _check_norm(np.where(big, 0, got), e, ref, np.where(big, 0, slack))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 144, 128), (20, 272, 144), (64, 656, 512), (300, 272, 656), (1300, 400, 272),
+                                   (777, 1360, 1104), (5000, 1296, 528)])
+@pytest.mark.parametrize("out", ["bf16", "fp32", "fp8"])
+def test_linear_gelu_in_ragged_blocks(M, N, K, out):
+    """GELU where the last block of columns is not full, values far below zero among them, on both kernels."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8
+    rng = np.random.default_rng(M + N + K)
+    a, sa, av = _operand(rng, M, K, scale=2)
+    w, sw, wv = _operand(rng, N, K, scale=1 / math.sqrt(K))
+    bias = (3 * rng.standard_normal(N)).astype(np.float32)
+    bias[-16:] = -40                                   # GELU is zero in fp32 here
+    y = F8.linear(av, wv, bias)
+    ref = F8.gelu(y)
+    rel, tail = {"fp32": (8 * E32, 8 * E32), "bf16": (1.3e-5, 5e-11), "fp8": (2.6e-4, 2e-8)}[out]   # as in test_linear
+    slack = 1.13 * (_acc_slack(av, wv, K) + 2 * E32 * (np.abs(y) + np.abs(bias))) + rel * np.abs(ref) + tail * np.abs(y)
+    r = linear_fp8(a, sa, w, sw, bias=_t(bias), out_dtype=out, gelu=True)
+    if out == "fp8":
+        got, e = _deq(*r)
+        _check_norm(got, e, ref, slack)
+    else:
+        got = r.double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= slack + HALF[out] * (np.abs(ref) + slack))
