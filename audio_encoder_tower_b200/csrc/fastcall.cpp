@@ -54,6 +54,21 @@ bool sizes_fit(int64_t rows, int64_t cols) { return rows <= INT32_MAX && cols <=
 
 PyObject* answer(int code) { return PyLong_FromLong(code); }
 
+// The status of a C call made without the interpreter's lock: a launch waits for as long as the
+// device's queue is full, and other Python threads run meanwhile.
+struct WithoutLock {
+  PyThreadState* state = PyEval_SaveThread();
+  ~WithoutLock() { PyEval_RestoreThread(state); }
+};
+template <typename F> PyObject* answer_of(F&& call) {
+  int code;
+  {
+    WithoutLock unlocked;
+    code = call();
+  }
+  return answer(code);
+}
+
 // No C++ exception leaves a function that Python calls: one means that a tensor is unusual.
 template <PyObject* (*f)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* v, Py_ssize_t n) {
@@ -87,9 +102,14 @@ PyObject* linear(PyObject* const* v, Py_ssize_t n) {
     if (t < 0 || v[6] != Py_None || !is_matrix(*out, M, N, dev)) return answer(kUnusual);
     kind = t == ENC_DTYPE_BF16 ? ENC_FP8_OUT_BF16 : ENC_FP8_OUT_FP32;
   }
-  return answer(enc_linear_fp8(a->data_ptr(), tensor(v[1])->data_ptr(), w->data_ptr(), tensor(v[3])->data_ptr(), bias,
-                               out->data_ptr(), out_scales, kind, (int32_t)M, (int32_t)N, (int32_t)K, v[7] == Py_True,
-                               nullptr, c10::cuda::getCurrentCUDAStream(dev).stream()));
+  const void *ap = a->data_ptr(), *as = tensor(v[1])->data_ptr(), *wp = w->data_ptr(), *ws = tensor(v[3])->data_ptr();
+  void* op = out->data_ptr();
+  const int gelu = v[7] == Py_True;
+  const auto stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+  return answer_of([&] {
+    return enc_linear_fp8(ap, as, wp, ws, bias, op, out_scales, kind, (int32_t)M, (int32_t)N, (int32_t)K, gelu, nullptr,
+                          stream);
+  });
 }
 
 // norm(kind, x, gamma, beta, delta, eps, x_out, q, scales): kind an enc_norm_kind; x_out None without a delta
@@ -118,9 +138,15 @@ PyObject* norm(PyObject* const* v, Py_ssize_t n) {
     if (!t || dtype_of(*t) != xt || !is_matrix(*t, rows, d, dev)) return answer(kUnusual);
     x_out = t->data_ptr();
   }
-  return answer(enc_norm_fp8((int32_t)PyLong_AsLong(v[0]), x->data_ptr(), xt, d, delta, dt, d, gamma, beta,
-                             (float)PyFloat_AS_DOUBLE(v[5]), (int32_t)rows, (int32_t)d, x_out, d, q->data_ptr(),
-                             s->data_ptr(), c10::cuda::getCurrentCUDAStream(dev).stream()));
+  const int32_t kind = (int32_t)PyLong_AsLong(v[0]);
+  const float eps = (float)PyFloat_AS_DOUBLE(v[5]);
+  const void* xp = x->data_ptr();
+  void *qp = q->data_ptr(), *sp = s->data_ptr();
+  const auto stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+  return answer_of([&] {
+    return enc_norm_fp8(kind, xp, xt, d, delta, dt, d, gamma, beta, eps, (int32_t)rows, (int32_t)d, x_out, d, qp, sp,
+                        stream);
+  });
 }
 
 // quantize(x, q, scales)
@@ -134,8 +160,10 @@ PyObject* quantize(PyObject* const* v, Py_ssize_t n) {
   if (dev != c10::cuda::current_device() || xt < 0 || !sizes_fit(rows, cols) || !is_matrix(*x, rows, cols, dev) ||
       !is_fp8(q, s, rows, cols, dev))
     return answer(kUnusual);
-  return answer(enc_quantize_fp8(x->data_ptr(), xt, cols, (int32_t)rows, (int32_t)cols, q->data_ptr(), s->data_ptr(),
-                                 c10::cuda::getCurrentCUDAStream(dev).stream()));
+  const void* xp = x->data_ptr();
+  void *qp = q->data_ptr(), *sp = s->data_ptr();
+  const auto stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+  return answer_of([&] { return enc_quantize_fp8(xp, xt, cols, (int32_t)rows, (int32_t)cols, qp, sp, stream); });
 }
 
 PyMethodDef methods[] = {

@@ -690,3 +690,37 @@ def test_linear_gelu_in_ragged_blocks(M, N, K, out):
     else:
         got = r.double().cpu().numpy()
         assert np.all(np.abs(got - ref) <= slack + HALF[out] * (np.abs(ref) + slack))
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """With the device's queue full a call waits for it to drain; other Python threads go on meanwhile."""
+    import threading
+    import time
+    import torch
+    from audio_encoder_tower_b200 import binding, quantize_fp8
+    x = _t(np.ones((64, 256), np.float32))
+    q, s = quantize_fp8(x)
+    assert binding._fast_quantize(x, q, s) == 0
+    torch.cuda.synchronize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.001)
+
+    thread = threading.Thread(target=tick)
+    thread.start()
+    torch.cuda._sleep(2_000_000_000)            # a second and more
+    t0, longest = time.perf_counter(), 0.0
+    for _ in range(6000):
+        t = time.perf_counter()
+        quantize_fp8(x, q, s)
+        longest = max(longest, time.perf_counter() - t)
+    t1 = time.perf_counter()
+    stop.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert longest > 0.3                        # a call did wait
+    seen = [t0] + [t for t in ticks if t0 < t < t1] + [t1]
+    assert max(b - a for a, b in zip(seen, seen[1:])) < longest / 2
