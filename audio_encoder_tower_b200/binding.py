@@ -415,6 +415,8 @@ def _bind_torch():
     load_library()
     try:
         from . import _fastcall
+        if getattr(_fastcall, "torch_version", None) != torch.__version__:
+            raise ImportError("built against another PyTorch")
         _fast_quantize, _fast_norm, _fast_linear = _fastcall.quantize, _fastcall.norm, _fastcall.linear
     except ImportError:
         _fast_quantize = _fast_norm = _fast_linear = lambda *args: -1

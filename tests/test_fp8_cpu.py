@@ -200,3 +200,55 @@ def test_enum_values_match_the_header():
                         ("ENC_FP8_OUT_FP8", B.ENC_FP8_OUT_FP8), ("ENC_FP8_OUT_RESID", B.ENC_FP8_OUT_RESID)):
         assert f"{name} = {value}" in src
     assert ctypes.sizeof(ctypes.c_int64) == 8
+
+
+# ------------------------------------------------------- the short call's module
+@pytest.mark.parametrize("compiler", ["fails", "missing"])
+def test_library_builds_where_the_short_call_does_not(lib, tmp_path, monkeypatch, compiler):
+    """build() warns and takes an old module away; the library is there and the calls go through ctypes."""
+    bin_dir = tmp_path / "bin"
+    bin_dir.mkdir()
+    if compiler == "fails":
+        (bin_dir / "g++").write_text("#!/bin/sh\necho no c10_cuda >&2\nexit 1\n")
+        (bin_dir / "g++").chmod(0o755)
+    module = tmp_path / "_fastcall.so"
+    module.write_bytes(b"of another build")
+    monkeypatch.setattr(build, "FASTCALL", str(module))
+    monkeypatch.setattr(build, "FASTCALL_STAMP", str(tmp_path / "stamp"))
+    monkeypatch.setenv("PATH", str(bin_dir))
+    with pytest.warns(UserWarning, match="ctypes"):
+        assert build.build() == build.LIB
+    assert not module.exists()
+    with pytest.raises((OSError, RuntimeError)):
+        build.build_fastcall()
+
+
+def test_short_call_is_rebuilt_for_another_pytorch(lib, tmp_path, monkeypatch):
+    calls = []
+
+    def compiled(cmd, **_):
+        calls.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "wb").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", compiled)
+    monkeypatch.setattr(build, "FASTCALL", str(tmp_path / "_fastcall.so"))
+    monkeypatch.setattr(build, "FASTCALL_STAMP", str(tmp_path / "stamp"))
+    assert build.build_fastcall() and build.build_fastcall() and len(calls) == 1
+    assert any(torch.__version__ in arg for arg in calls[0])
+    (tmp_path / "stamp").write_text("0.0.1")
+    assert build.build_fastcall() and len(calls) == 2
+
+
+def test_short_call_of_another_pytorch_is_not_used(lib, monkeypatch):
+    import types
+    import audio_encoder_tower_b200 as package
+    B._bind_torch()
+    assert B._fast_quantize.__name__ == "quantize"
+    other = types.SimpleNamespace(torch_version="0.0.1", quantize=None, norm=None, linear=None)
+    with monkeypatch.context() as m:
+        m.setattr(package, "_fastcall", other)
+        B._bind_torch()
+        assert B._fast_quantize(1, 2, 3) == -1 and B._fast_norm() == -1 and B._fast_linear() == -1
+    B._bind_torch()
+    assert B._fast_quantize.__name__ == "quantize"
