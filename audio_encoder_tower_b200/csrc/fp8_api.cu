@@ -91,8 +91,8 @@ enc_status enc_linear_fp8(const void* A, const void* a_scales, const void* W, co
   if (out_kind < ENC_FP8_OUT_BF16 || out_kind > ENC_FP8_OUT_RESID || M < 0 || N <= 0 || K <= 0)
     return ENC_ERR_INVALID_ARG;
   if (gelu && out_kind == ENC_FP8_OUT_RESID) return ENC_ERR_INVALID_ARG;
-  // tiles reach past the last row and column by up to 255: their indexes stay in 32 bits
-  if (K % 16 || N % 16 || M > INT32_MAX - 512 || N > INT32_MAX - 512 ||
+  // tiles reach past the last row and column by up to 255, and blocks past K by 127: their indexes stay in 32 bits
+  if (K % 16 || N % 16 || K > INT32_MAX - 512 || M > INT32_MAX - 512 || N > INT32_MAX - 512 ||
       (int64_t)(M / 256 + 1) * (N / 256 + 1) > INT32_MAX / 2)
     return ENC_ERR_UNSUPPORTED;
   if (M == 0) return ENC_OK;

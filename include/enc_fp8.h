@@ -93,8 +93,8 @@ typedef enum enc_fp8_out {
  *   bias          fp32 [N], 16-byte aligned, or NULL
  *   out           as out_kind says, 16-byte aligned, overlapping none of the others
  *   out_scales    ENC_FP8_OUT_FP8 only, [M, enc_fp8_scale_pitch(N)]
- *   K, N          multiples of 16; at least 16. M and N at most 2^31 - 513, at most 2^30
- *                 tiles of 256 x 256
+ *   K, N          multiples of 16; at least 16. M, N and K at most 2^31 - 513, at most
+ *                 2^30 tiles of 256 x 256
  *   status        device int (may be NULL) set to ENC_ERR_TIMEOUT if a bounded
  *                 wait inside the kernel runs out
  * The order in which an element's products are summed depends on M, N and K alone:

@@ -252,3 +252,9 @@ def test_short_call_of_another_pytorch_is_not_used(lib, monkeypatch):
         assert B._fast_quantize(1, 2, 3) == -1 and B._fast_norm() == -1 and B._fast_linear() == -1
     B._bind_torch()
     assert B._fast_quantize.__name__ == "quantize"
+
+
+@pytest.mark.parametrize("K", [2 ** 31 - 512, 2 ** 31 - 128, 2 ** 31 - 112, 2 ** 31 - 16])
+def test_linear_refuses_a_depth_past_its_range(lib, K):
+    """Past 2^31 - 128 the number of blocks overflowed to a negative one, and nothing was summed."""
+    assert lib.enc_linear_fp8(A, A, A, A, None, A, None, 0, 4, 128, K, 0, None, None) == UNSUPPORTED
