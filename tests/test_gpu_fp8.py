@@ -724,3 +724,103 @@ def test_other_threads_run_while_a_launch_waits():
     assert longest > 0.3                        # a call did wait
     seen = [t0] + [t for t in ticks if t0 < t < t1] + [t1]
     assert max(b - a for a, b in zip(seen, seen[1:])) < longest / 2
+
+
+@pytest.mark.parametrize("d", [2208, 4016, 5120, 5648, 7168, 8192])
+@pytest.mark.parametrize("x_type,delta_type", [("bf16", None), ("fp32", None), ("bf16", "bf16"), ("fp32", "fp32")])
+def test_norm_many_wide_rows(d, x_type, delta_type):
+    """The kernel for many rows of more than 16 blocks against the one for rows that run at once (here 100 of them: a
+    block of four warps each, and an SM holds two), and its last rows against float64."""
+    import torch
+    from audio_encoder_tower_b200 import norm_fp8
+    rows = 1501
+    T = {"bf16": torch.bfloat16, "fp32": torch.float32}
+    g = torch.Generator("cuda").manual_seed(d)
+    x = (3 * torch.randn(rows, d, device="cuda", dtype=torch.float32, generator=g) + 0.5).to(T[x_type])
+    delta = None
+    if delta_type is not None:
+        delta = torch.randn(rows, d, device="cuda", dtype=torch.float32, generator=g).to(T[delta_type])
+    gamma, beta = (torch.randn(d, device="cuda", dtype=torch.float32, generator=g) for _ in range(2))
+    for kind in ("rms", "layer"):
+        q, s, o = norm_fp8(x, gamma, beta, delta=delta, kind=kind)
+        for r in range(0, rows, 100):
+            e = min(r + 100, rows)
+            few = norm_fp8(x[r:e], gamma, beta, delta=None if delta is None else delta[r:e], kind=kind)
+            assert all(torch.equal(a.view(torch.uint8), b[r:e].view(torch.uint8)) for a, b in zip(few, (q, s, o), strict=True))
+        st = o[-20:].double().cpu().numpy()
+        gm, bt = gamma.double().cpu().numpy(), beta.double().cpu().numpy()
+        got, e = _deq(q[-20:], s[-20:])
+        mean = st.mean(1, keepdims=True) if kind == "layer" else 0
+        sd = np.sqrt(((st - mean) ** 2).mean(1, keepdims=True) + 1e-5)
+        slack = 60 * E32 * (np.abs(st) / sd * np.abs(gm) + np.abs(bt))       # as in test_norm
+        if kind == "layer":
+            slack = slack + 80 * E32 * np.abs(st).mean(1, keepdims=True) / sd * np.abs(gm)
+        _check_norm(got, e, F8.norm(st, gm, bt, kind), slack)
+
+
+def test_captured_with_branches():
+    """A capture in which the calls follow a join of two streams, a memset and a copy, replayed on new data."""
+    import torch
+    from audio_encoder_tower_b200 import linear_fp8, norm_fp8, quantize_fp8
+    rng = np.random.default_rng(53)
+    x, y = (_t(rng.standard_normal((700, 640)).astype(np.float32)) for _ in range(2))
+    gamma = _t((1 + 0.1 * rng.standard_normal(640)).astype(np.float32))
+    w, sw, _ = _operand(rng, 640, 640, scale=1 / 25)
+    side = torch.cuda.Stream()
+    out, copy = torch.empty_like(x), torch.empty_like(x)
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        a, sa = quantize_fp8(x)
+        with torch.cuda.stream(side):
+            b, sb, _ = norm_fp8(y, gamma)
+            h = linear_fp8(b, sb, w, sw, out_dtype="fp32")
+        main.wait_stream(side)
+        n, sn, _ = norm_fp8(h, gamma, delta=x)             # after a join
+        out.zero_()
+        linear_fp8(a, sa, w, sw, resid=out)                # after a memset
+        copy.copy_(out)
+        m, sm = quantize_fp8(copy)                         # after a copy
+        linear_fp8(n, sn, w, sw, resid=out)
+        linear_fp8(m[:20], sm[:20], w, sw, resid=out[:20])
+        return (a, b, h, n, m)                             # kept until the graph has run
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = run()
+    for k in (1, 2, 3):
+        x.copy_(_t(rng.standard_normal((700, 640)).astype(np.float32)))
+        y.copy_(x * k)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+    del kept
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_linear_deepest(M):
+    """K past 2^28: the rows of both operands lie further apart than 32 bits of bytes reach, and the sums are short."""
+    import torch
+    from audio_encoder_tower_b200 import binding, linear_fp8
+    K, N = 2 ** 28 + 48, 16
+    if torch.cuda.mem_get_info()[0] < 20 * 2 ** 30:
+        pytest.skip("needs 20 GB")
+    mats = []
+    for rows in (M, N):
+        q = torch.zeros(rows, K, dtype=torch.uint8, device="cuda")
+        q[:, K - 48:] = 0x38                                          # 1.0: the last block, of 48 columns
+        q[:, ::2 ** 26] = 0x40                                        # 2.0: in blocks of every CTA's share
+        s = torch.full((rows, binding.fp8_scale_pitch(K)), 127, dtype=torch.uint8, device="cuda")
+        s[:, -(-K // 128) - 1] = 127 + torch.arange(rows, device="cuda", dtype=torch.uint8) % 8
+        mats += [q.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = linear_fp8(*mats, out_dtype="fp32", status=status).double().cpu().numpy()
+    last = 2.0 ** (np.arange(M) % 8)[:, None] * 2.0 ** (np.arange(N) % 8)[None, :]
+    # 2^28 is the fifth multiple of 2^26, the first column of the last block
+    assert np.array_equal(got, 4 * 4.0 + last * (47 + 4)) and int(status) == 0
