@@ -239,7 +239,8 @@ norm_fp8_kernel(const T* x, T* x_out, const NormParams p) {
   const int d = p.d;
   auto inside = [&](int i) { return i < NV - kRagged || c0 + i * kStep < d; };
   Raw4<T> raw[NV] = {};
-  const T* xr = x + row * p.ldx + c0;
+  // A warp past the last row reads gamma in the place of its row: all of x may be being written, in place
+  const T* xr = (live ? x + row * p.ldx : reinterpret_cast<const T*>(p.gamma)) + c0;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (inside(i)) raw[i] = load4(xr + i * kStep);

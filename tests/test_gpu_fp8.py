@@ -824,3 +824,20 @@ def test_linear_deepest(M):
     last = 2.0 ** (np.arange(M) % 8)[:, None] * 2.0 ** (np.arange(N) % 8)[None, :]
     # 2^28 is the fifth multiple of 2^26, the first column of the last block
     assert np.array_equal(got, 4 * 4.0 + last * (47 + 4)) and int(status) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 7, 6002])
+def test_norm_in_place_with_warps_past_the_last_row(rows):
+    """In place the stream is read once, by the warps that own its rows: those past the last row read none of it, and
+    give the same bits as a call that writes the stream elsewhere."""
+    import torch
+    from audio_encoder_tower_b200 import norm_fp8
+    rng = np.random.default_rng(rows)
+    x = _t(rng.standard_normal((rows, 1280)).astype(np.float32))
+    delta = _t(rng.standard_normal((rows, 1280)).astype(np.float32), torch.bfloat16)
+    gamma = _t(rng.standard_normal(1280).astype(np.float32))
+    apart = norm_fp8(x, gamma, delta=delta)
+    for _ in range(3):
+        y = x.clone()
+        q, s, o = norm_fp8(y, gamma, delta=delta, x_out=y)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(apart, (q, s, o), strict=True))
