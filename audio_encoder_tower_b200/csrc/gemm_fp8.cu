@@ -80,9 +80,12 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint4
 // has read them there, which it therefore does first. Until then the MMAs of the tile's other
 // half run, over the first kEarly blocks of K (as N = 128 each; from there on N = 256), so that
 // the tensor cores do not wait for the epilogue between tiles.
-// Measured (one B200): 24000 x 5120 x 1280 with GELU to e4m3 137 to 141 us (2,290 TFLOP/s), 18737 x
-// 3840 x 1280 to bf16 82 us, 24000 x 1280 x 5120 122 us (2,580). Power bounds these: the SM clock is
-// 1.47 GHz with the tensor pipe busy 64% of the cycles at K = 1280 and 1.25 GHz with 86% at 5120.
+// Measured (one B200, 20 launches in a replayed graph): 24000 x 5120 x 1280 with GELU to e4m3 136 to
+// 137 us (2,300 TFLOP/s), 18737 x 3840 x 1280 to bf16 82 us, 24000 x 1280 x 5120 to fp32 124 us (2,540).
+// Called for longer the clock falls: 164 to 166 us and 98 to 99. Power bounds these: the SM clock is
+// 1.46 GHz with the tensor pipe busy 63% of the cycles at K = 1280 and 1.25 GHz with 86% at 5120.
+// Added to fp32 (24000 x 1280 x 1280) 59 us: plain fp32 stores of that shape take 45, HBM is 60% busy;
+// the difference is the reductions in L2.
 // Smaller grids are bound by an SM's intake from L2, about 58 bytes a cycle: 32 KB per 512 cycles of
 // MMAs for a full unit.
 constexpr int kEpiWarp0 = 4;

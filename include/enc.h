@@ -88,7 +88,9 @@ typedef enum enc_status {
  * without the flag. dtype must be ENC_DTYPE_BF16: weights, mel and out are bf16.
  * Against the exact result the output is seven to ten times as far as in bf16 (e4m3
  * holds 4 significant bits, bf16 holds 8): 1.2 to 1.8 % of its norm instead of 0.18 %
- * on a two-block tower with N(0, 0.02) weights.
+ * on a two-block tower with N(0, 0.02) weights. It grows with the depth: after the 32
+ * blocks of Whisper-large's geometry, on random weights, the output differs from the bf16
+ * forward's by 8.8 % of its norm.
  */
 #define ENC_FLAG_FP8 2u
 

@@ -46,6 +46,7 @@ ENC_API int32_t enc_fp8_scale_pitch(int32_t cols);
  *   x       [rows, cols] of x_dtype (enc_dtype), row stride ldx elements (>= cols);
  *           16-byte aligned, ldx a multiple of 4
  *   cols    a multiple of 16, <= 65536; rows * ceil(cols / 128) below 2^31 - 4096
+ * q and scales overlap neither x nor each other.
  */
 ENC_API enc_status enc_quantize_fp8(const void *x, int32_t x_dtype, int64_t ldx, int32_t rows, int32_t cols,
                                     void *q, void *scales, cudaStream_t stream);
@@ -97,9 +98,9 @@ typedef enum enc_fp8_out {
  *                 2^30 tiles of 256 x 256
  *   status        device int (may be NULL) set to ENC_ERR_TIMEOUT if a bounded
  *                 wait inside the kernel runs out
- * The order in which an element's products are summed depends on M, N and K alone:
- * the same call gives the same bits every time (ENC_FP8_OUT_RESID as well: every
- * element is added to once). NaN in a row of A or W (an element or a scale) makes that
+ * The order in which an element's products are summed depends on M, N, K and the
+ * device's number of SMs alone: on a device the same call gives the same bits every time
+ * (ENC_FP8_OUT_RESID as well: every element is added to once). NaN in a row of A or W (an element or a scale) makes that
  * row or column of the output NaN; sums past fp32's range are not finite, and NaN in
  * e4m3, with GELU too. (In bf16 and fp32 GELU takes a sum of minus infinity to its limit,
  * zero.)
