@@ -129,7 +129,8 @@ __device__ __forceinline__ void gelu_fp32_2(float& x0, float& x1) {
 
 // GELU for an e4m3 result, on packed pairs: max(x, 0) - |x| 2^G(|x|) as gelu_fast2, with
 // G = log2 Phi(-a) from a minimax polynomial of degree 5 over [0, 5.5] (relative error of the
-// result there at most 2.5e-4, a 250th of half an e4m3 step). Beyond, the polynomial keeps
+// result there at most 2.5e-4, a 250th of half an e4m3 step: of 24000 x 5120 values 0.08% round to
+// the neighbour of erff's; degree 7 makes that 0.006% and 137.5 us 140.4). Beyond, the polynomial keeps
 // falling, so no clamp is needed: the result is within 1.9e-8 |x| of max(x, 0), as GELU is.
 __device__ __forceinline__ void gelu_e4m3_2(float& x0, float& x1) {
   constexpr float c0 = -1.000359058380127f, c1 = -1.1462607383728027f, c2 = -0.4696812331676483f,
